@@ -558,6 +558,124 @@ fp8_status fp8_linear_fwd_cached(const void* X, int64_t M, int64_t K, int64_t N,
                                  fp8_scaling x_scaling, const uint8_t* w8, fp8_layout lw, const fp8_scale_t* sw,
                                  uint8_t* x8, fp8_scale_t* sx, void* Y, hipStream_t stream);
 
+/*
+ * ---- Block-scaled FP8: one power-of-two scale for each block of 128 ----
+ *
+ * A block-scaled matrix [rows, cols] holds for each row, and each block of
+ * 128 consecutive columns of it, FP8 codes and one scale:
+ *   bias  = floor(log2(fmt_max / max |x| over the block)), clamped to
+ *           [-126, 126]; 0 for a block that is all zero or holds an
+ *           infinity or a NaN,
+ *   code  = fp8(clamp(x * 2^bias)), to nearest even (NaN stays NaN),
+ *   value = code * 2^-bias.
+ * It is stored as
+ *   codes   row-major bytes, row pitch = cols rounded up to 128 (the pad
+ *           holds zero codes): fp8_block_codes_bytes;
+ *   scales  the bytes 127 - bias, block-major: block kb's bytes start at
+ *           kb * (rows rounded up to 128), and within them row r is at
+ *           (r & ~127) + 8 (r % 16) + (r % 128) / 16:
+ *           fp8_block_scales_bytes. Bytes of rows past the last one are
+ *           not written and affect no result.
+ * A product takes its blocks along its own reduction, so a matrix that is
+ * used in two products of different reductions is quantised in its row form
+ * and in its transposed form (blocks down its columns), from one read.
+ *
+ * bf16 inputs are row-major with a row pitch in elements (any value >= 0;
+ * 0 repeats one row) and need no alignment but their own 2 bytes; bf16
+ * outputs are dense. Codes, scales and workspaces are 16-B aligned. A
+ * dimension is at most 2^23 - 128, and a matrix has fewer than 2^31
+ * scales; beyond: FP8_ERR_UNSUPPORTED. Sizes of 0 are valid: an empty
+ * reduction gives zeros. Workspaces hold nothing from one call to the next
+ * except `kept`, from a forward to its backward. Calls with equal
+ * arguments give equal bits: sums are added in an order fixed by the sizes.
+ */
+
+/* Bytes of the codes and of the scales of a block-scaled [rows, cols]. */
+size_t fp8_block_codes_bytes(int64_t rows, int64_t cols);
+size_t fp8_block_scales_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Block-scaled form(s) of a bf16 matrix x [rows, cols], row pitch ldx, in
+ * one pass: row_codes / row_scales the row form [rows, cols], t_codes /
+ * t_scales the transposed form [cols, rows]. Either pair may be NULL.
+ */
+fp8_status fp8_block_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ldx, fp8_fmt fmt,
+                              uint8_t* row_codes, uint8_t* row_scales, uint8_t* t_codes, uint8_t* t_scales,
+                              hipStream_t stream);
+
+/* The values of a block-scaled matrix, rounded to bf16 (exact unless a
+ * value is below bf16's normal range); ldo: the output's row pitch. */
+fp8_status fp8_block_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, fp8_fmt fmt,
+                                void* out_bf16, int64_t ldo, hipStream_t stream);
+
+/*
+ * C [M, N] (bf16, row pitch ldc) = A B^T on block-scaled A [M, R] and
+ * B [N, R], summed in FP32 and rounded once. ws: optional workspace that
+ * lets a product with few output tiles split its reduction
+ * (fp8_block_gemm_workspace_bytes; 0: it would not); smaller or NULL: no
+ * split, the same result up to the order of the FP32 sums.
+ */
+size_t fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t R);
+fp8_status fp8_block_gemm(const uint8_t* A, const uint8_t* sA, fp8_fmt fa, const uint8_t* B, const uint8_t* sB,
+                          fp8_fmt fb, int64_t M, int64_t N, int64_t R, void* C_bf16, int64_t ldc, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/* Gradients wanted of a block-scaled linear or MLP (flags). */
+#define FP8_BLOCK_NEED_DX 1  /* of the input */
+#define FP8_BLOCK_NEED_DW 2  /* of the weight (MLP: of the gate and up weight) */
+#define FP8_BLOCK_NEED_DW2 4 /* MLP: of the down weight */
+
+/*
+ * One linear on block-scaled operands: Y [M, N] = X [M, K] W [K, N] with X
+ * and W in E4M3; dX = dY W^T and dW = X^T dY with dY in E5M2. The forward
+ * leaves in `kept` the 8-bit forms that the wanted gradients need, the
+ * backward (same sizes and flags) reads them; `scratch` is either call's
+ * own. fp8_block_linear_bytes gives the sizes of kept and of each scratch.
+ */
+fp8_status fp8_block_linear_bytes(int64_t M, int64_t K, int64_t N, int flags, size_t* kept, size_t* fwd_scratch,
+                                  size_t* bwd_scratch);
+fp8_status fp8_block_linear_fwd(const void* X_bf16, int64_t ldx, const void* W_bf16, int64_t ldw, int64_t M, int64_t K,
+                                int64_t N, int flags, void* kept, size_t kept_bytes, void* scratch,
+                                size_t scratch_bytes, void* Y_bf16, hipStream_t stream);
+fp8_status fp8_block_linear_bwd(const void* dY_bf16, int64_t lddy, int64_t M, int64_t K, int64_t N, int flags,
+                                const void* kept, size_t kept_bytes, void* scratch, size_t scratch_bytes, void* dX_bf16,
+                                void* dW_bf16, hipStream_t stream);
+
+/* The forward on a weight quantised once: w_codes / w_scales the
+ * transposed E4M3 form [N, K] of W [K, N] (fp8_block_quantize). */
+size_t fp8_block_linear_cached_bytes(int64_t M, int64_t K, int64_t N);
+fp8_status fp8_block_linear_fwd_cached(const void* X_bf16, int64_t ldx, int64_t M, int64_t K, int64_t N,
+                                       const uint8_t* w_codes, const uint8_t* w_scales, void* scratch,
+                                       size_t scratch_bytes, void* Y_bf16, hipStream_t stream);
+
+/*
+ * SwiGLU: h = gate sigmoid(gate) up, all [rows, cols]. kept (or NULL)
+ * receives the E4M3 block-scaled gate and up; the backward computes at
+ * those: with g, u their values and s = sigmoid(g),
+ *   dgate = dh u s (1 + g (1 - s)),  dup = dh g s   (either may be NULL).
+ */
+size_t fp8_swiglu_kept_bytes(int64_t rows, int64_t cols);
+fp8_status fp8_swiglu_fwd(const void* gate_bf16, int64_t ldg, const void* up_bf16, int64_t ldu, int64_t rows,
+                          int64_t cols, void* h_bf16, void* kept, size_t kept_bytes, hipStream_t stream);
+fp8_status fp8_swiglu_bwd(const void* dh_bf16, int64_t lddh, int64_t rows, int64_t cols, const void* kept,
+                          size_t kept_bytes, void* dgate_bf16, void* dup_bf16, hipStream_t stream);
+
+/*
+ * A SwiGLU MLP: Y [M, K] = h Wd [F, K], h = SwiGLU of the halves of
+ * X [M, K] Wgu [K, 2 F] (rounded to bf16). h is quantised from its FP32
+ * value, the gradient of the gate and up values likewise (E5M2); the
+ * backward recomputes h from the 8-bit gate and up. Blocks along the 2 F
+ * columns start anew at column F. Buffers as for the linear.
+ */
+fp8_status fp8_block_mlp_bytes(int64_t M, int64_t K, int64_t F, int flags, size_t* kept, size_t* fwd_scratch,
+                               size_t* bwd_scratch);
+fp8_status fp8_block_mlp_fwd(const void* X_bf16, int64_t ldx, const void* Wgu_bf16, int64_t ldwgu, const void* Wd_bf16,
+                             int64_t ldwd, int64_t M, int64_t K, int64_t F, int flags, void* kept, size_t kept_bytes,
+                             void* scratch, size_t scratch_bytes, void* Y_bf16, hipStream_t stream);
+fp8_status fp8_block_mlp_bwd(const void* dY_bf16, int64_t lddy, int64_t M, int64_t K, int64_t F, int flags,
+                             const void* kept, size_t kept_bytes, void* scratch, size_t scratch_bytes, void* dX_bf16,
+                             void* dWgu_bf16, void* dWd_bf16, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,8 @@ LIB_PATH = os.environ.get("FP8LIN_LIB", os.path.join(_HERE, "lib", "libfp8lin.so
 c_i64 = ctypes.c_int64
 c_int = ctypes.c_int
 c_vp = ctypes.c_void_p
+c_sz = ctypes.c_size_t
+c_szp = ctypes.POINTER(ctypes.c_size_t)
 
 # name -> (restype, argtypes); mirrors include/fp8lin.h
 SIGNATURES = {
@@ -48,6 +50,28 @@ SIGNATURES = {
     "fp8_adam_step_spec": (c_int, [c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                    c_vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                    ctypes.c_float, ctypes.c_int32, c_vp]),
+    "fp8_block_codes_bytes": (c_sz, [c_i64, c_i64]),
+    "fp8_block_scales_bytes": (c_sz, [c_i64, c_i64]),
+    "fp8_block_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "fp8_block_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
+    "fp8_block_gemm_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "fp8_block_gemm": (c_int, [c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_sz,
+                               c_vp]),
+    "fp8_block_linear_bytes": (c_int, [c_i64, c_i64, c_i64, c_int, c_szp, c_szp, c_szp]),
+    "fp8_block_linear_fwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp, c_sz,
+                                     c_vp, c_vp]),
+    "fp8_block_linear_bwd": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp, c_sz, c_vp, c_vp,
+                                     c_vp]),
+    "fp8_block_linear_cached_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "fp8_block_linear_fwd_cached": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "fp8_swiglu_kept_bytes": (c_sz, [c_i64, c_i64]),
+    "fp8_swiglu_fwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]),
+    "fp8_swiglu_bwd": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_sz, c_vp, c_vp, c_vp]),
+    "fp8_block_mlp_bytes": (c_int, [c_i64, c_i64, c_i64, c_int, c_szp, c_szp, c_szp]),
+    "fp8_block_mlp_fwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp,
+                                  c_sz, c_vp, c_vp]),
+    "fp8_block_mlp_bwd": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp, c_sz, c_vp, c_vp, c_vp,
+                                  c_vp]),
 }
 
 FP8_E4M3, FP8_E5M2 = 0, 1
@@ -56,6 +80,7 @@ FP8_OK, FP8_ERR_INVALID, FP8_ERR_UNSUPPORTED, FP8_ERR_HIP = 0, 1, 2, 3
 FLAG_NONFINITE, FLAG_ZERO, FLAG_CLAMPED = 1, 2, 4
 FP8_SCALING_AMAX, FP8_SCALING_FIXED = 0, 1
 FP8_SPLIT_AUTO, FP8_SPLIT_NEVER, FP8_SPLIT_TAIL = 0, 1, 2
+FP8_BLOCK_NEED_DX, FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2 = 1, 2, 4
 ABI_VERSION = 13
 FP8_NOALLOC_SCRATCH_BYTES = 128 * 2 * 65536 * 4   # the device scratch of fp8_gemm_noalloc
 
