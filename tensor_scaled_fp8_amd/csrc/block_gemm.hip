@@ -100,11 +100,11 @@ __device__ inline int tile_bytes(int64_t rows, int64_t r0, int tile, int64_t pit
 // through the wave's own LDS so that a store writes whole row pieces: 16
 // rows at a time, 32 FN bytes a row, chunks of 16 bytes swizzled.
 template <int FM, int FN, typename Acc>
-__device__ inline void store_wave(lds_u8* wst, const Acc& acc, uint16_t* c, int64_t ldc, int M, int N, int m0,
+__device__ inline void store_wave(lds_u8* wst, int t, const Acc& acc, uint16_t* c, int64_t ldc, int M, int N, int m0,
                                   int n0) {
   constexpr int kChunks = 2 * FN;              // 16-byte chunks of a row
   constexpr int kRowsPer = 64 / kChunks;       // rows a store instruction covers
-  const int lane = threadIdx.x & 63, r16 = lane & 15, G = lane >> 4;
+  const int lane = t & 63, r16 = lane & 15, G = lane >> 4;
   const int dc = lane % kChunks, dr = lane / kChunks;
   static_for<FM>([&](auto M_) {
     constexpr int mi = decltype(M_)::value;
@@ -116,26 +116,28 @@ __device__ inline void store_wave(lds_u8* wst, const Acc& acc, uint16_t* c, int6
                        __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2))};
       const int chunk = (2 * ni + (G >> 1)) ^ (r16 & (kChunks - 1));
       *(lds_u32x2*)(wst + r16 * (16 * kChunks) + 16 * chunk + 8 * (G & 1)) = p;
+      // a few blocks at a time, which bounds how many accumulators are
+      // moved out of the accumulation registers at once
+      if constexpr (ni % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     });
     // one wave's LDS accesses are processed in order: no barrier
     asm volatile("" ::: "memory");
     static_for<16 / kRowsPer>([&](auto K_) {
       const int r = dr + kRowsPer * decltype(K_)::value;
-      const u32x4 v = *(const lds_u32x4*)(wst + r * (16 * kChunks) + 16 * (dc ^ (r & (kChunks - 1))));
+      const lds_u8* src = wst + r * (16 * kChunks) + 16 * (dc ^ (r & (kChunks - 1)));
       const int row = m0 + 16 * mi + r, col = n0 + 8 * dc;
       if (row < M) {
         uint16_t* d = c + (int64_t)row * ldc + col;
         if (col + 8 <= N) {
-          __builtin_nontemporal_store(v, (u32x4_a2*)d);
+          __builtin_nontemporal_store(*(const lds_u32x4*)src, (u32x4_a2*)d);
         } else {
-          static_for<8>([&](auto E_) {
-            constexpr int e = decltype(E_)::value;
-            if (col + e < N) d[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-          });
+#pragma clang loop unroll(disable)
+          for (int e = 0; e < N - col; ++e) d[e] = ((const LDS_AS uint16_t*)src)[e];
         }
       }
     });
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   });
 }
 
@@ -285,13 +287,267 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
     return;
   }
   store_wave<FM, FN>(
-      l8 + w * (16 * 32 * FN), [&](auto I_, auto J_) { return acc[decltype(I_)::value][decltype(J_)::value]; }, p.c, p.ldc,
+      l8 + w * (16 * 32 * FN), t, [&](auto I_, auto J_) { return acc[decltype(I_)::value][decltype(J_)::value]; }, p.c, p.ldc,
       p.M, p.N, m0 + wm * (BM / 2), n0 + wn * (BN / 2));
 }
 
 template <int FMT_A, int FMT_B, int BM, int BN, int SLOTS>
 __global__ __launch_bounds__(256) void block_gemm_kernel(Problem p) {
   gemm_tile<FMT_A, FMT_B, BM, BN, SLOTS>(p);
+}
+
+// ---- the 256 x 256 tile --------------------------------------------------
+// 4 waves of 128 x 128 (8 x 8 blocks, 256 accumulators a lane), one wave a
+// SIMD, so nothing but the wave's own schedule hides a load or an LDS read:
+// a stage's fragments are read under the MFMAs of the stage before it, in
+// place where the MFMAs that used a register are past, double-buffered in
+// registers otherwise. A is held in two slots of LDS and B in three (160
+// KB, all of a CU's); one barrier opens each stage. The slots are objects
+// of their own, always named at compile time, so that the compiler can tell
+// a slot that is read from one with loads in flight.
+constexpr int kBig = 256;
+constexpr int kOpBytes = kBig * kBlk;  // 32 KB: one operand's part of a stage
+__shared__ uint4 g_a0[kOpBytes / 16];
+__shared__ uint4 g_a1[kOpBytes / 16];
+__shared__ uint4 g_b0[kOpBytes / 16];
+__shared__ uint4 g_b1[kOpBytes / 16];
+__shared__ uint4 g_b2[kOpBytes / 16];
+template <int S>
+__device__ inline lds_u8* a_slot() {
+  if constexpr (S % 2 == 0) return (lds_u8*)g_a0;
+  else return (lds_u8*)g_a1;
+}
+template <int S>
+__device__ inline lds_u8* b_slot() {
+  if constexpr (S % 3 == 0) return (lds_u8*)g_b0;
+  else if constexpr (S % 3 == 1) return (lds_u8*)g_b1;
+  else return (lds_u8*)g_b2;
+}
+
+// c += the scaled product of a 16 x 16 x 128 piece, scale bytes SB and SA of
+// the two words. In asm so that the result is tied to the accumulator's
+// registers: left free to take others, with all 256 accumulation registers
+// in use, the compiler spilled hundreds to memory. Its operands come from
+// LDS reads and loads (the compiler waits for those) and nothing reads a
+// result before the s_nop after the loop.
+template <int FMT_B, int FMT_A, int SB, int SA>
+__device__ __forceinline__ void mfma_into(f32x4& c, const v8i& b, const v8i& a, uint32_t sb, uint32_t sa) {
+  asm volatile(
+      "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:%9 blgp:%10"
+      : "+a"(c)
+      : "v"(b), "v"(a), "v"(sb), "v"(sa), "n"(SB & 1), "n"(SA & 1), "n"(SB >> 1), "n"(SA >> 1), "n"(FMT_B), "n"(FMT_A));
+}
+
+template <int FMT_A, int FMT_B>
+__device__ __forceinline__ void gemm_tile_big(const Problem& p) {
+  const int ntiles = p.tiles_m * p.tiles_n;
+  const int split = blockIdx.x / ntiles;
+  int tm, tn;
+  tile_origin(blockIdx.x - split * ntiles, p.tiles_m, p.tiles_n, tm, tn);
+  const int m0 = tm * kBig, n0 = tn * kBig;
+  const int k0 = (int)((int64_t)split * p.nk / p.splits), k1 = (int)((int64_t)(split + 1) * p.nk / p.splits);
+  const int nk = k1 - k0;
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w >> 1, wn = w & 1;
+
+  // loads: wave w fills rows 64 w .. 64 w + 63 of either part, 8 rows an
+  // instruction (layout as in gemm_tile)
+  const uint8_t* const abase = p.a + (int64_t)m0 * p.pa + (int64_t)k0 * kBlk;
+  const uint8_t* const bbase = p.b + (int64_t)n0 * p.pb + (int64_t)k0 * kBlk;
+  const int abytes = tile_bytes(p.M, m0, kBig, p.pa) - k0 * kBlk, bbytes = tile_bytes(p.N, n0, kBig, p.pb) - k0 * kBlk;
+  int offa[8], offb[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 8 * (8 * w + i) + (lane >> 3);
+    // 32-bit products, kept apart from the sum by an empty asm: fused into
+    // a 64-bit multiply-add, each offset would occupy a register pair
+    int pa = row * (int)p.pa, pb = row * (int)p.pb;
+    asm volatile("" : "+v"(pa), "+v"(pb));
+    offa[i] = pa + 16 * ((lane & 7) ^ swz(row));
+    offb[i] = pb + 16 * ((lane & 7) ^ swz(row));
+  }
+  // loads i0 .. i0 + n - 1 of a stage's part; a stage past the last reads
+  // zeros through a resource of no bytes, which keeps the counts in flight
+  auto issue_a = [&](lds_u8* sl, int s, auto I0_, auto N_) {
+    constexpr int i0 = decltype(I0_)::value, n = decltype(N_)::value;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)abase, (short)0, s < nk ? abytes : 0, kRsrcWord3);
+    const int ko = s < nk ? s * kBlk : 0;
+#pragma unroll
+    for (int i = i0; i < i0 + n; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(sl + (8 * w + i) * 1024), 16, offa[i], ko, 0, 0);
+  };
+  auto issue_b = [&](lds_u8* sl, int s, auto I0_, auto N_) {
+    constexpr int i0 = decltype(I0_)::value, n = decltype(N_)::value;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)bbase, (short)0, s < nk ? bbytes : 0, kRsrcWord3);
+    const int ko = s < nk ? s * kBlk : 0;
+#pragma unroll
+    for (int i = i0; i < i0 + n; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(sl + (8 * w + i) * 1024), 16, offb[i], ko, 0, 0);
+  };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  using C8 = std::integral_constant<int, 8>;
+
+  // scales: a lane's eight bytes of A's and of B's 128 rows
+  const int asz = (int)(p.sra * p.nk), bsz = (int)(p.srb * p.nk);
+  const int soffa = m0 + 128 * wm + 8 * (lane & 15), soffb = n0 + 128 * wn + 8 * (lane & 15);
+  auto scales = [&](int s, u32x2& xa, u32x2& xb) {
+    const int kb = max(min(k0 + s, p.nk - 1), 0);  // past the last: read again, not used
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)p.sa, (short)0, asz, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)p.sb, (short)0, bsz, kRsrcWord3);
+    xa = __builtin_amdgcn_raw_buffer_load_b64(ra, soffa, kb * (int)p.sra, 0);
+    xb = __builtin_amdgcn_raw_buffer_load_b64(rb, soffb, kb * (int)p.srb, 0);
+  };
+
+  const int fr = lane & 15, fG = lane >> 4;
+  int foff[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) foff[j] = fr * kBlk + (((2 * fG + j) ^ swz(fr)) << 4);
+  auto frag = [&](const lds_u8* q, auto M_) -> v8i {
+    constexpr int m = decltype(M_)::value;
+    const u32x4 lo = *(const lds_u32x4*)(q + foff[0] + 2048 * m);
+    const u32x4 hi = *(const lds_u32x4*)(q + foff[1] + 2048 * m);
+    return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  };
+  const int a_row0 = 128 * wm * kBlk, b_row0 = 128 * wn * kBlk;
+
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+
+  // fragments (P = parity of the stage): A blocks 0..5 in fa, 6 and 7 in
+  // fa67[P]; B blocks 0..3 in fb, 4..7 in fb47[P] (176 registers); scales
+  // in xa[P], xb[P]
+  v8i fa[6], fa67[2][2], fb[4], fb47[2][4];
+  u32x2 xa[2], xb[2];
+  scales(0, xa[0], xb[0]);
+  issue_a(a_slot<0>(), 0, C0{}, C8{});
+  issue_b(b_slot<0>(), 0, C0{}, C8{});
+  issue_a(a_slot<1>(), 1, C0{}, C8{});
+  issue_b(b_slot<1>(), 1, C0{}, C8{});
+  issue_b(b_slot<2>(), 2, C0{}, C8{});
+  // the accumulators are zeroed while the first loads fly
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+  wait_vmcnt<24>();
+  block_sync_lds();
+  static_for<6>([&](auto M_) { fa[decltype(M_)::value] = frag(a_slot<0>() + a_row0, M_); });
+  static_for<2>([&](auto M_) {
+    constexpr int m = decltype(M_)::value;
+    fa67[0][m] = frag(a_slot<0>() + a_row0, std::integral_constant<int, 6 + m>{});
+  });
+  static_for<4>([&](auto N_) {
+    constexpr int n = decltype(N_)::value;
+    fb[n] = frag(b_slot<0>() + b_row0, N_);
+    fb47[0][n] = frag(b_slot<0>() + b_row0, std::integral_constant<int, 4 + n>{});
+  });
+
+  // One stage (J: its index mod 6, for compile-time slots and registers).
+  // Loads of A of stage s + 2 and B of s + 3 go into the slots of stage s,
+  // whose fragments are in registers; reads are of stage s + 1, spread one
+  // or two after each MFMA. A fragment register is refilled only after the
+  // MFMAs that read it.
+  auto stage = [&](auto J_, int s) {
+    constexpr int J = decltype(J_)::value, P = J & 1, Q = P ^ 1;
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<8>();   // stage s + 1 and its scales landed; B of s + 2 may fly
+    block_sync_lds();  // everyone's loads landed, everyone's reads of stage s are done
+    __builtin_amdgcn_sched_barrier(0);
+    const lds_u8* na = a_slot<J + 1>() + a_row0;
+    const lds_u8* nb = b_slot<J + 1>() + b_row0;
+    auto mfma = [&](auto N_, const v8i& a, auto M_) {
+      constexpr int n = decltype(N_)::value, m = decltype(M_)::value;
+      if constexpr (n < 4)
+        mfma_into<FMT_B, FMT_A, n & 3, m & 3>(acc[m][n], fb[n], a, xb[P][n >> 2], xa[P][m >> 2]);
+      else
+        mfma_into<FMT_B, FMT_A, n & 3, m & 3>(acc[m][n], fb47[P][n - 4], a, xb[P][n >> 2], xa[P][m >> 2]);
+    };
+    // row blocks 0..3: the next scales, A's loads; A block mi - 1 in place
+    // and the double-buffered blocks
+    static_for<4>([&](auto MI_) {
+      constexpr int mi = decltype(MI_)::value;
+      static_for<8>([&](auto N_) {
+        constexpr int n = decltype(N_)::value;
+        mfma(N_, fa[mi], MI_);
+        if constexpr (n == 0 && mi == 0) scales(s + 1, xa[Q], xb[Q]);
+        if constexpr (n == 1 || n == 5) issue_a(a_slot<J>(), s + 2, std::integral_constant<int, 2 * mi + (n >> 2)>{}, C1{});
+        if constexpr (n == 2) fb47[Q][mi] = frag(nb, std::integral_constant<int, 4 + mi>{});
+        if constexpr (n == 4 && mi >= 2) fa67[Q][mi - 2] = frag(na, std::integral_constant<int, 4 + mi>{});
+        if constexpr (n == 6 && mi >= 1) fa[mi - 1] = frag(na, std::integral_constant<int, mi - 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    // column pairs over rows 4, 5: B's loads; A block 3 in place
+    static_for<4>([&](auto C_) {
+      constexpr int c = decltype(C_)::value;
+      static_for<4>([&](auto D_) {
+        constexpr int d = decltype(D_)::value;
+        using Nc = std::integral_constant<int, 2 * c + (d >> 1)>;
+        mfma(Nc{}, fa[4 + (d & 1)], std::integral_constant<int, 4 + (d & 1)>{});
+        if constexpr (d == 1) issue_b(b_slot<J>(), s + 3, C_, C1{});
+        if constexpr (d == 2 && c == 0) fa[3] = frag(na, std::integral_constant<int, 3>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    // column pairs over rows 6, 7: B's loads; A blocks 4, 5 and B blocks
+    // 0..3 in place
+    static_for<4>([&](auto C_) {
+      constexpr int c = decltype(C_)::value;
+      static_for<4>([&](auto D_) {
+        constexpr int d = decltype(D_)::value;
+        using Nc = std::integral_constant<int, 2 * c + (d >> 1)>;
+        mfma(Nc{}, fa67[P][d & 1], std::integral_constant<int, 6 + (d & 1)>{});
+        if constexpr (d == 1) issue_b(b_slot<J>(), s + 3, std::integral_constant<int, 4 + c>{}, C1{});
+        if constexpr (c == 0 && d != 1 && d != 3) fa[4 + (d >> 1)] = frag(na, std::integral_constant<int, 4 + (d >> 1)>{});
+        if constexpr (c >= 1 && c <= 2 && (d == 0 || d == 2))
+          fb[2 * c - 2 + (d >> 1)] = frag(nb, std::integral_constant<int, 2 * c - 2 + (d >> 1)>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+  };
+  int s = 0;
+  for (; s + 6 <= nk; s += 6)
+    static_for<6>([&](auto J_) { stage(J_, s + decltype(J_)::value); });
+  const int rest = nk - s;
+  static_for<5>([&](auto J_) {
+    if (decltype(J_)::value < rest) stage(J_, s + decltype(J_)::value);
+  });
+  asm volatile("s_nop 15\n\ts_nop 15");  // the last MFMAs' results may be read
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+  wait_vmcnt<0>();
+  block_sync_lds();
+
+  // (the thread index through an empty asm keeps this addressing out of the
+  // k-loop, where registers are full)
+  int te = t;
+  asm volatile("" : "+v"(te));
+  if (p.splits > 1) {
+    float* d = p.part + ((int64_t)split * ntiles + (tm * p.tiles_n + tn)) * (kBig * kBig) + 4 * te;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *(f32x4*)(d + 1024 * (i * 8 + j)) = acc[i][j];
+    return;
+  }
+  store_wave<8, 8>(
+      (lds_u8*)g_b2 + w * 8192, te, [&](auto I_, auto J_) { return acc[decltype(I_)::value][decltype(J_)::value]; }, p.c,
+      p.ldc, p.M, p.N, m0 + 128 * wm, n0 + 128 * wn);
+}
+
+template <int FMT_A, int FMT_B>
+__global__ __launch_bounds__(256, 1) void block_gemm_big_kernel(Problem p) {
+  gemm_tile_big<FMT_A, FMT_B>(p);
 }
 
 // sums the partials of one row block (blockIdx.y) of a tile in split order
@@ -312,7 +568,7 @@ __global__ __launch_bounds__(256) void block_gemm_join_kernel(Problem p) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[j] += *(const f32x4*)(s + 1024 * j);
   }
-  store_wave<1, FN>((lds_u8*)lds + w * (16 * 32 * FN), [&](auto, auto J_) { return acc[decltype(J_)::value]; }, p.c,
+  store_wave<1, FN>((lds_u8*)lds + w * (16 * 32 * FN), t, [&](auto, auto J_) { return acc[decltype(J_)::value]; }, p.c,
                     p.ldc, p.M, p.N, tm * BM + (w >> 1) * (BM / 2) + 16 * i, tn * BN + (w & 1) * (BN / 2));
 }
 
@@ -321,7 +577,14 @@ struct Plan {
   int bm, bn, splits;
 };
 inline Plan plan(int64_t M, int64_t N, int64_t nk, bool may_split) {
-  Plan q{128, 128, 1};
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+  Plan q{256, 256, 1};
+  if (big >= 200) return q;
+  if (big >= 100 && nk >= 16) {
+    if (may_split) q.splits = 2;
+    return q;
+  }
+  q = {128, 128, 1};
   const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
   if (may_split && tiles < 256) {
     int64_t s = 512 / tiles;
@@ -332,10 +595,15 @@ inline Plan plan(int64_t M, int64_t N, int64_t nk, bool may_split) {
 }
 
 template <int FA, int FB>
-hipError_t run(const Problem& p, hipStream_t st) {
+hipError_t run(const Problem& p, int bm, hipStream_t st) {
   const int ntiles = p.tiles_m * p.tiles_n;
-  block_gemm_kernel<FA, FB, 128, 128, 2><<<dim3(ntiles * p.splits), 256, 0, st>>>(p);
-  if (p.splits > 1) block_gemm_join_kernel<128, 128><<<dim3(ntiles, 4), 256, 0, st>>>(p);
+  if (bm == kBig) {
+    block_gemm_big_kernel<FA, FB><<<dim3(ntiles * p.splits), 256, 0, st>>>(p);
+    if (p.splits > 1) block_gemm_join_kernel<256, 256><<<dim3(ntiles, 8), 256, 0, st>>>(p);
+  } else {
+    block_gemm_kernel<FA, FB, 128, 128, 2><<<dim3(ntiles * p.splits), 256, 0, st>>>(p);
+    if (p.splits > 1) block_gemm_join_kernel<128, 128><<<dim3(ntiles, 4), 256, 0, st>>>(p);
+  }
   return hipGetLastError();
 }
 
@@ -370,8 +638,8 @@ hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipS
   p.tiles_n = (int)((N + q.bn - 1) / q.bn);
   p.splits = q.splits;
   p.part = (float*)ws;
-  if (g.fa == FP8_E5M2) return g.fb == FP8_E5M2 ? run<1, 1>(p, st) : run<1, 0>(p, st);
-  return g.fb == FP8_E5M2 ? run<0, 1>(p, st) : run<0, 0>(p, st);
+  if (g.fa == FP8_E5M2) return g.fb == FP8_E5M2 ? run<1, 1>(p, q.bm, st) : run<1, 0>(p, q.bm, st);
+  return g.fb == FP8_E5M2 ? run<0, 1>(p, q.bm, st) : run<0, 0>(p, q.bm, st);
 }
 
 }  // namespace fp8lin
