@@ -26,18 +26,31 @@ from ._lib import (FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2, FP8_BLOCK_NEED_DX, che
 from .binding import _fmt, _stream
 
 BLOCK = 128
+_BF16, _U8 = torch.bfloat16, torch.uint8
+
+# The stream's handle alone: a Stream object around it costs 2 us a call,
+# as much as a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(t: torch.Tensor) -> int:
+    return _stream(t) if _raw_stream is None else _raw_stream(t.get_device())
 
 
 def _round(n: int) -> int:
     return -(-n // BLOCK) * BLOCK
 
 
-def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(pointer, row pitch) of a 2-D bf16 device matrix with contiguous rows."""
+def _check_bf16(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (no CPU path exists)")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(pointer, row pitch) of a 2-D bf16 device matrix with contiguous rows."""
+    _check_bf16(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     ld, step = t.stride()
@@ -46,33 +59,40 @@ def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
     return t.data_ptr(), ld
 
 
+def _as_rows(t: torch.Tensor, name: str):
+    """t [..., n] bf16 as a matrix with contiguous rows (a view where it can
+    be): (the matrix, pointer, row pitch, rows, columns)."""
+    _check_bf16(t, name)
+    if t.dim() != 2:
+        t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        t = t.contiguous()
+        ld = cols
+    return t, t.data_ptr(), ld, rows, cols
+
+
 def _same_device(a: torch.Tensor, b: torch.Tensor, name: str) -> None:
     if a.device != b.device:
         raise ValueError(f"{name} must be on {a.device}, got {b.device}")
 
 
-def _as_rows(t: torch.Tensor) -> torch.Tensor:
-    """t [..., n] as a matrix with contiguous rows (a view where it can be)."""
-    if t.dim() != 2:
-        t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
-    return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
-
-
 class BlockTensor:
-    """A stored matrix [rows, cols]: codes (uint8 [rows, cols rounded up to
-    128]), scales (uint8, in the library's order) and the FP8 format."""
+    """A stored matrix [rows, cols] of an FP8 format: data (uint8) holds the
+    codes, [rows, cols rounded up to 128], then the scales in the library's
+    order."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "fmt")
+    __slots__ = ("data", "rows", "cols", "fmt")
 
-    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, fmt: int):
-        self.codes, self.scales, self.rows, self.cols, self.fmt = codes, scales, rows, cols, fmt
+    def __init__(self, data: torch.Tensor, rows: int, cols: int, fmt: int):
+        self.data, self.rows, self.cols, self.fmt = data, rows, cols, fmt
 
     @classmethod
     def empty(cls, rows: int, cols: int, fmt, device) -> "BlockTensor":
         pitch = _round(cols)
-        codes = torch.empty((rows, pitch), dtype=torch.uint8, device=device)
-        scales = torch.empty((pitch // BLOCK, _round(rows)), dtype=torch.uint8, device=device)
-        return cls(codes, scales, rows, cols, _fmt(fmt))
+        return cls(torch.empty(rows * pitch + _round(rows) * (pitch // BLOCK), dtype=_U8, device=device), rows, cols,
+                   _fmt(fmt))
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -80,16 +100,33 @@ class BlockTensor:
 
     @property
     def device(self):
-        return self.codes.device
+        return self.data.device
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return self.data.numel()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        """uint8 [rows, cols rounded up to 128], a view."""
+        pitch = _round(self.cols)
+        return self.data[:self.rows * pitch].view(self.rows, pitch)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """uint8 [blocks, rows rounded up to 128] in the library's order, a view."""
+        pitch = _round(self.cols)
+        return self.data[self.rows * pitch:].view(pitch // BLOCK, _round(self.rows))
+
+    def pointers(self) -> Tuple[int, int]:
+        p = self.data.data_ptr()
+        return p, p + self.rows * _round(self.cols)
 
     def biases(self) -> torch.Tensor:
         """The scaling bias of each block: int32 [rows, blocks]; a code stands for code * 2^-bias."""
-        nb, sr = self.scales.shape
-        s = self.scales.reshape(nb, sr // BLOCK, 16, 8).transpose(2, 3).reshape(nb, sr)
+        s = self.scales
+        nb, sr = s.shape
+        s = s.reshape(nb, sr // BLOCK, 16, 8).transpose(2, 3).reshape(nb, sr)
         return 127 - s[:, :self.rows].t().to(torch.int32)
 
     def dequantize(self, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -105,27 +142,29 @@ def fp8_block_quantize(x: torch.Tensor, fmt="e4m3", rowwise: bool = True, transp
     f = _fmt(fmt)
     if not rowwise and not transposed:
         raise ValueError("neither form is wanted")
-    q = BlockTensor.empty(rows, cols, f, x.device) if rowwise else None
-    qt = BlockTensor.empty(cols, rows, f, x.device) if transposed else None
-    check(load().fp8_block_quantize(p, rows, cols, ld, f, q.codes.data_ptr() if rowwise else None,
-                                    q.scales.data_ptr() if rowwise else None,
-                                    qt.codes.data_ptr() if transposed else None,
-                                    qt.scales.data_ptr() if transposed else None, _stream(x)), "fp8_block_quantize")
+    q = qt = c = s = ct = st = None
+    if rowwise:
+        q = BlockTensor.empty(rows, cols, f, x.device)
+        c, s = q.pointers()
+    if transposed:
+        qt = BlockTensor.empty(cols, rows, f, x.device)
+        ct, st = qt.pointers()
+    check(load().fp8_block_quantize(p, rows, cols, ld, f, c, s, ct, st, _on(x)), "fp8_block_quantize")
     return q, qt
 
 
 def fp8_block_dequantize(q: BlockTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a stored matrix, bf16 [rows, cols]; out: any row pitch."""
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=torch.bfloat16, device=q.codes.device)
+        out = torch.empty((q.rows, q.cols), dtype=_BF16, device=q.data.device)
         p, ld = out.data_ptr(), q.cols
     else:
         if tuple(out.shape) != (q.rows, q.cols):
             raise ValueError("out has the wrong shape")
         p, ld = _rows(out, "out")
-        _same_device(q.codes, out, "out")
-    check(load().fp8_block_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, q.fmt, p, ld,
-                                      _stream(out)), "fp8_block_dequantize")
+        _same_device(q.data, out, "out")
+    c, s = q.pointers()
+    check(load().fp8_block_dequantize(c, s, q.rows, q.cols, q.fmt, p, ld, _on(out)), "fp8_block_dequantize")
     return out
 
 
@@ -133,20 +172,30 @@ def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] =
     """C [M, N] (bf16) = A B^T of stored A [M, R] and B [N, R], any formats."""
     if a.cols != b.cols:
         raise ValueError(f"reduction mismatch: A {a.shape}, B {b.shape}")
-    _same_device(a.codes, b.codes, "B")
+    _same_device(a.data, b.data, "B")
     M, N, R = a.rows, b.rows, a.cols
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = torch.empty((M, N), dtype=_BF16, device=a.device)
     if tuple(out.shape) != (M, N):
         raise ValueError("out has the wrong shape")
     p, ld = _rows(out, "out")
-    _same_device(a.codes, out, "out")
-    lib = load()
-    nb = lib.fp8_block_gemm_workspace_bytes(M, N, R)
-    ws = torch.empty(nb, dtype=torch.uint8, device=a.device) if nb else None
-    check(lib.fp8_block_gemm(a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, b.codes.data_ptr(), b.scales.data_ptr(),
-                             b.fmt, M, N, R, p, ld, ws.data_ptr() if nb else None, nb, _stream(out)), "fp8_block_gemm")
+    _same_device(a.data, out, "out")
+    nb = _gemm_bytes(M, N, R)
+    ws = torch.empty(nb, dtype=_U8, device=a.device) if nb else None
+    check(load().fp8_block_gemm(*a.pointers(), a.fmt, *b.pointers(), b.fmt, M, N, R, p, ld,
+                                ws.data_ptr() if nb else None, nb, _on(out)), "fp8_block_gemm")
     return out
+
+
+# Sizes of workspaces, by the sizes of the call
+@functools.lru_cache(maxsize=4096)
+def _gemm_bytes(M: int, N: int, R: int) -> int:
+    return load().fp8_block_gemm_workspace_bytes(M, N, R)
+
+
+@functools.lru_cache(maxsize=4096)
+def _cached_bytes(M: int, K: int, N: int) -> int:
+    return load().fp8_block_linear_cached_bytes(M, K, N)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -158,37 +207,41 @@ def _bytes(entry: str, a: int, b: int, c: int, flags: int) -> Tuple[int, int, in
 
 
 def _space(n: int, device) -> torch.Tensor:
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=_U8, device=device)
 
 
-def _flags(ctx) -> int:
-    need = ctx.needs_input_grad
-    return sum(f for f, n in zip((FP8_BLOCK_NEED_DX, FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2), need) if n)
+def _flags(needs) -> int:
+    return sum(f for f, n in zip((FP8_BLOCK_NEED_DX, FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2), needs) if n)
 
 
-def _grad_rows(dy: torch.Tensor) -> torch.Tensor:
-    if dy.dtype != torch.bfloat16:
-        dy = dy.to(torch.bfloat16)
-    return _as_rows(dy)
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+def _as_grad(dy: torch.Tensor, name: str):
+    return _as_rows(dy if dy.dtype is _BF16 else dy.to(_BF16), name)
+
+
+def _linear_fwd(X, W, flags):
+    X2, px, ldx, M, K = _as_rows(X, "X")
+    W2, pw, ldw, _, N = _as_rows(W, "W")
+    nk, nf, _ = _bytes("fp8_block_linear_bytes", M, K, N, flags)
+    dev = X.device
+    kept = _space(nk, dev) if flags else None
+    scratch = _space(nf, dev)
+    Y = torch.empty((*X.shape[:-1], N), dtype=_BF16, device=dev)
+    check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, flags, kept.data_ptr() if flags else None, nk,
+                                      scratch.data_ptr(), nf, Y.data_ptr(), _on(X)), "fp8_block_linear_fwd")
+    return Y, kept, (M, K, N)
 
 
 class _BlockLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W):
-        X2, W2 = _as_rows(X), _as_rows(W)
-        (px, ldx), (pw, ldw) = _rows(X2, "X"), _rows(W2, "W")
-        M, K = X2.shape
-        N = W2.shape[1]
-        flags = _flags(ctx)
-        nk, nf, _ = _bytes("fp8_block_linear_bytes", M, K, N, flags)
-        kept = _space(nk, X.device)
-        scratch = _space(nf, X.device)
-        Y = torch.empty((*X.shape[:-1], N), dtype=torch.bfloat16, device=X.device)
-        check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, flags, kept.data_ptr(), nk, scratch.data_ptr(), nf,
-                                          Y.data_ptr(), _stream(X)), "fp8_block_linear_fwd")
-        if flags:
-            ctx.save_for_backward(kept)
-            ctx.flags, ctx.size, ctx.lead = flags, (M, K, N), X.shape[:-1]
+        flags = _flags(ctx.needs_input_grad)
+        Y, kept, ctx.size = _linear_fwd(X, W, flags)
+        ctx.save_for_backward(kept)
+        ctx.flags, ctx.lead = flags, X.shape[:-1]
         return Y
 
     @staticmethod
@@ -197,16 +250,15 @@ class _BlockLinearFn(torch.autograd.Function):
         kept, = ctx.saved_tensors
         M, K, N = ctx.size
         flags = ctx.flags
-        dY2 = _grad_rows(dY)
-        p, ld = _rows(dY2, "dY")
+        dY, p, ld, _, _ = _as_grad(dY, "dY")
+        dev = dY.device
         nk, _, nb = _bytes("fp8_block_linear_bytes", M, K, N, flags)
-        scratch = _space(nb, dY.device)
-        new = dict(dtype=torch.bfloat16, device=dY.device)
-        dX = torch.empty((*ctx.lead, K), **new) if flags & FP8_BLOCK_NEED_DX else None
-        dW = torch.empty((K, N), **new) if flags & FP8_BLOCK_NEED_DW else None
+        scratch = _space(nb, dev)
+        dX = torch.empty((*ctx.lead, K), dtype=_BF16, device=dev) if flags & FP8_BLOCK_NEED_DX else None
+        dW = torch.empty((K, N), dtype=_BF16, device=dev) if flags & FP8_BLOCK_NEED_DW else None
         check(load().fp8_block_linear_bwd(p, ld, M, K, N, flags, kept.data_ptr(), nk, scratch.data_ptr(), nb,
                                           None if dX is None else dX.data_ptr(), None if dW is None else dW.data_ptr(),
-                                          _stream(dY)), "fp8_block_linear_bwd")
+                                          _on(dY)), "fp8_block_linear_bwd")
         return dX, dW
 
 
@@ -217,7 +269,7 @@ def block_linear(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     if X.dim() < 1 or W.dim() != 2 or X.shape[-1] != W.shape[0]:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
     _same_device(X, W, "W")
-    return _BlockLinearFn.apply(X, W)
+    return _BlockLinearFn.apply(X, W) if _wants_grad(X, W) else _linear_fwd(X, W, 0)[0]
 
 
 class BlockLinear(torch.nn.Module):
@@ -225,7 +277,7 @@ class BlockLinear(torch.nn.Module):
 
     def __init__(self, in_features: int, out_features: int, device=None):
         super().__init__()
-        self.weight = torch.nn.Parameter(torch.empty((in_features, out_features), dtype=torch.bfloat16, device=device))
+        self.weight = torch.nn.Parameter(torch.empty((in_features, out_features), dtype=_BF16, device=device))
         torch.nn.init.normal_(self.weight, std=0.02)
 
     def forward(self, x):
@@ -244,16 +296,16 @@ def fp8_block_linear_fwd_cached(X: torch.Tensor, w: BlockTensor, Y: Optional[tor
     N = w.rows
     if w.cols != K or w.fmt != 0:
         raise ValueError(f"X {tuple(X.shape)} does not go with the stored weight {w.shape} (E4M3, transposed)")
-    _same_device(X, w.codes, "w")
+    _same_device(X, w.data, "w")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    elif tuple(Y.shape) != (M, N) or Y.dtype != torch.bfloat16 or not Y.is_contiguous() or Y.device != X.device:
+        Y = torch.empty((M, N), dtype=_BF16, device=X.device)
+    elif tuple(Y.shape) != (M, N) or Y.dtype is not _BF16 or not Y.is_contiguous() or Y.device != X.device:
         raise ValueError("Y must be a contiguous bf16 [M, N] on X's device")
-    lib = load()
-    nb = lib.fp8_block_linear_cached_bytes(M, K, N)
+    nb = _cached_bytes(M, K, N)
     scratch = _space(nb, X.device)
-    check(lib.fp8_block_linear_fwd_cached(p, ld, M, K, N, w.codes.data_ptr(), w.scales.data_ptr(), scratch.data_ptr(),
-                                          nb, Y.data_ptr(), _stream(X)), "fp8_block_linear_fwd_cached")
+    c, s = w.pointers()
+    check(load().fp8_block_linear_fwd_cached(p, ld, M, K, N, c, s, scratch.data_ptr(), nb, Y.data_ptr(), _on(X)),
+          "fp8_block_linear_fwd_cached")
     return Y
 
 
@@ -262,33 +314,37 @@ class BlockInferenceLinear(torch.nn.Module):
 
     def __init__(self, W: torch.Tensor):
         super().__init__()
-        q = prepare_block_weight(W)
-        self.register_buffer("codes", q.codes)
-        self.register_buffer("scales", q.scales)
-        self.in_features, self.out_features = q.cols, q.rows
+        self.register_buffer("weight", prepare_block_weight(W).data)
+        self.in_features, self.out_features = W.shape
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        w = BlockTensor(self.codes, self.scales, self.out_features, self.in_features, 0)
-        return fp8_block_linear_fwd_cached(_as_rows(x), w).reshape(*x.shape[:-1], self.out_features)
+        w = BlockTensor(self.weight, self.out_features, self.in_features, 0)
+        return fp8_block_linear_fwd_cached(_as_rows(x, "x")[0], w).reshape(*x.shape[:-1], self.out_features)
+
+
+def _swiglu_fwd(gate, up, keep):
+    g2, pg, ldg, rows, cols = _as_rows(gate, "gate")
+    u2, pu, ldu, _, _ = _as_rows(up, "up")
+    dev = gate.device
+    n = _swiglu_bytes(rows, cols) if keep else 0
+    kept = _space(n, dev) if keep else None
+    h = torch.empty(gate.shape, dtype=_BF16, device=dev)
+    check(load().fp8_swiglu_fwd(pg, ldg, pu, ldu, rows, cols, h.data_ptr(), kept.data_ptr() if n else None, n,
+                                _on(gate)), "fp8_swiglu_fwd")
+    return h, kept, (rows, cols)
+
+
+@functools.lru_cache(maxsize=4096)
+def _swiglu_bytes(rows: int, cols: int) -> int:
+    return load().fp8_swiglu_kept_bytes(rows, cols)
 
 
 class _SwigluFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up):
-        g2, u2 = _as_rows(gate), _as_rows(up)
-        (pg, ldg), (pu, ldu) = _rows(g2, "gate"), _rows(u2, "up")
-        rows, cols = g2.shape
-        lib = load()
-        n = 0
-        kept = None
-        if any(ctx.needs_input_grad):
-            n = lib.fp8_swiglu_kept_bytes(rows, cols)
-            kept = _space(n, gate.device)
-            ctx.save_for_backward(kept)
-            ctx.size, ctx.shape = (rows, cols), gate.shape
-        h = torch.empty(gate.shape, dtype=torch.bfloat16, device=gate.device)
-        check(lib.fp8_swiglu_fwd(pg, ldg, pu, ldu, rows, cols, h.data_ptr(), kept.data_ptr() if n else None, n,
-                                 _stream(gate)), "fp8_swiglu_fwd")
+        h, kept, ctx.size = _swiglu_fwd(gate, up, True)
+        ctx.save_for_backward(kept)
+        ctx.shape = gate.shape
         return h
 
     @staticmethod
@@ -296,14 +352,14 @@ class _SwigluFn(torch.autograd.Function):
     def backward(ctx, dh):
         kept, = ctx.saved_tensors
         rows, cols = ctx.size
-        dh2 = _grad_rows(dh)
-        p, ld = _rows(dh2, "dh")
-        new = dict(dtype=torch.bfloat16, device=dh.device)
-        dg = torch.empty(ctx.shape, **new) if ctx.needs_input_grad[0] else None
-        du = torch.empty(ctx.shape, **new) if ctx.needs_input_grad[1] else None
+        dh, p, ld, _, _ = _as_grad(dh, "dh")
+        dev = dh.device
+        need = ctx.needs_input_grad
+        dg = torch.empty(ctx.shape, dtype=_BF16, device=dev) if need[0] else None
+        du = torch.empty(ctx.shape, dtype=_BF16, device=dev) if need[1] else None
         check(load().fp8_swiglu_bwd(p, ld, rows, cols, kept.data_ptr(), kept.numel(),
                                     None if dg is None else dg.data_ptr(), None if du is None else du.data_ptr(),
-                                    _stream(dh)), "fp8_swiglu_bwd")
+                                    _on(dh)), "fp8_swiglu_bwd")
         return dg, du
 
 
@@ -314,26 +370,30 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     if gate.shape != up.shape or gate.dim() < 1:
         raise ValueError(f"shape mismatch: gate {tuple(gate.shape)}, up {tuple(up.shape)}")
     _same_device(gate, up, "up")
-    return _SwigluFn.apply(gate, up)
+    return _SwigluFn.apply(gate, up) if _wants_grad(gate, up) else _swiglu_fwd(gate, up, False)[0]
+
+
+def _mlp_fwd(X, Wgu, Wd, flags):
+    X2, px, ldx, M, K = _as_rows(X, "X")
+    G2, pg, ldg, _, _ = _as_rows(Wgu, "Wgu")
+    D2, pd, ldd, F, _ = _as_rows(Wd, "Wd")
+    dev = X.device
+    nk, nf, _ = _bytes("fp8_block_mlp_bytes", M, K, F, flags)
+    kept = _space(nk, dev) if flags else None
+    scratch = _space(nf, dev)
+    Y = torch.empty(X.shape, dtype=_BF16, device=dev)
+    check(load().fp8_block_mlp_fwd(px, ldx, pg, ldg, pd, ldd, M, K, F, flags, kept.data_ptr() if flags else None, nk,
+                                   scratch.data_ptr(), nf, Y.data_ptr(), _on(X)), "fp8_block_mlp_fwd")
+    return Y, kept, (M, K, F)
 
 
 class _BlockMlpFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, Wgu, Wd):
-        X2, G2, D2 = _as_rows(X), _as_rows(Wgu), _as_rows(Wd)
-        (px, ldx), (pg, ldg), (pd, ldd) = _rows(X2, "X"), _rows(G2, "Wgu"), _rows(D2, "Wd")
-        M, K = X2.shape
-        F = D2.shape[0]
-        flags = _flags(ctx)
-        nk, nf, _ = _bytes("fp8_block_mlp_bytes", M, K, F, flags)
-        kept = _space(nk, X.device)
-        scratch = _space(nf, X.device)
-        Y = torch.empty(X.shape, dtype=torch.bfloat16, device=X.device)
-        check(load().fp8_block_mlp_fwd(px, ldx, pg, ldg, pd, ldd, M, K, F, flags, kept.data_ptr(), nk,
-                                       scratch.data_ptr(), nf, Y.data_ptr(), _stream(X)), "fp8_block_mlp_fwd")
-        if flags:
-            ctx.save_for_backward(kept)
-            ctx.flags, ctx.size, ctx.shape = flags, (M, K, F), X.shape
+        flags = _flags(ctx.needs_input_grad)
+        Y, kept, ctx.size = _mlp_fwd(X, Wgu, Wd, flags)
+        ctx.save_for_backward(kept)
+        ctx.flags, ctx.shape = flags, X.shape
         return Y
 
     @staticmethod
@@ -342,16 +402,16 @@ class _BlockMlpFn(torch.autograd.Function):
         kept, = ctx.saved_tensors
         M, K, F = ctx.size
         flags = ctx.flags
-        dY2 = _grad_rows(dY)
-        p, ld = _rows(dY2, "dY")
+        dY, p, ld, _, _ = _as_grad(dY, "dY")
+        dev = dY.device
         nk, _, nb = _bytes("fp8_block_mlp_bytes", M, K, F, flags)
-        scratch = _space(nb, dY.device)
-        new = dict(dtype=torch.bfloat16, device=dY.device)
+        scratch = _space(nb, dev)
+        new = dict(dtype=_BF16, device=dev)
         dX = torch.empty(ctx.shape, **new) if flags & FP8_BLOCK_NEED_DX else None
         dWgu = torch.empty((K, 2 * F), **new) if flags & FP8_BLOCK_NEED_DW else None
         dWd = torch.empty((F, K), **new) if flags & FP8_BLOCK_NEED_DW2 else None
         check(load().fp8_block_mlp_bwd(p, ld, M, K, F, flags, kept.data_ptr(), nk, scratch.data_ptr(), nb,
-                                       *[None if t is None else t.data_ptr() for t in (dX, dWgu, dWd)], _stream(dY)),
+                                       *[None if t is None else t.data_ptr() for t in (dX, dWgu, dWd)], _on(dY)),
               "fp8_block_mlp_bwd")
         return dX, dWgu, dWd
 
@@ -365,7 +425,7 @@ def block_mlp(X: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor) -> torch.Ten
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wgu {tuple(Wgu.shape)}, Wd {tuple(Wd.shape)}")
     _same_device(X, Wgu, "Wgu")
     _same_device(X, Wd, "Wd")
-    return _BlockMlpFn.apply(X, Wgu, Wd)
+    return _BlockMlpFn.apply(X, Wgu, Wd) if _wants_grad(X, Wgu, Wd) else _mlp_fwd(X, Wgu, Wd, 0)[0]
 
 
 class BlockMLP(torch.nn.Module):
