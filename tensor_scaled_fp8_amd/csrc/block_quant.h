@@ -1,9 +1,13 @@
 // Device pieces shared by the block-scaled quantise and SwiGLU kernels.
 //
-// A 256-thread block holds a 128 x 128 tile as 8 x 8 patches in 32 bits:
-// thread t has rows 8 (t / 16) .. + 7, columns 8 (t % 16) .. + 7. A row's
-// block of 128 then lies in 16 neighbouring lanes, a column's in 16 lane
-// groups of all four waves.
+// Codes come straight from v_cvt_scalef32_pk_{fp8,bf8}_{bf16,f32}, which
+// divides by the scale and rounds once to nearest even: 2 elements an
+// instruction, no multiply, and bf16 inputs are never widened. Checked
+// against a multiply and the plain conversion: the same codes for every
+// bf16 value and scale. Maxima of bf16 are taken two at a time on their
+// magnitude bits. These kernels run each instruction once a workgroup, so
+// their code is kept small: an 18 KB body of branches cost 11 us a launch,
+// whatever the matrix, in instruction fetches alone.
 #pragma once
 
 #include "block.h"
@@ -11,12 +15,29 @@
 namespace fp8lin {
 
 typedef unsigned int bq_u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int bq_u32x2 __attribute__((ext_vector_type(2)));
 typedef bq_u32x4 bq_u32x4_a2 __attribute__((aligned(2)));  // a row of an odd pitch starts at any 2 bytes
+typedef bq_u32x2 bq_u32x2_a2 __attribute__((aligned(2)));
+typedef uint32_t bq_u32_a2 __attribute__((aligned(2)));
 typedef float bq_f32x2 __attribute__((ext_vector_type(2)));
+typedef float bq_f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bq_bf16x2 __attribute__((ext_vector_type(2)));
+typedef short bq_s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short bq_u16x2 __attribute__((ext_vector_type(2)));
 
-__device__ inline uint32_t mag_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 __device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ inline uint32_t pk_max(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(bq_u16x2, a),
+                                                                __builtin_bit_cast(bq_u16x2, b)));
+}
+__device__ inline uint32_t pk_min(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(bq_u16x2, a),
+                                                                __builtin_bit_cast(bq_u16x2, b)));
+}
+// |a| or |b|, the larger; a NaN if either is one (v_maximum3_f32)
+__device__ inline float nan_max(float a, float b) {
+  return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
+}
 
 // max over the 16 lanes that share t / 16 (one DPP row)
 __device__ inline uint32_t row16_max(uint32_t m) {
@@ -27,31 +48,59 @@ __device__ inline uint32_t row16_max(uint32_t m) {
   return m;
 }
 
-// four values at a scale to four codes; `odd`: the block holds an infinity
-// or a NaN (its scale is then 1), so values are clamped; a NaN stays one.
-// Elsewhere the scale keeps every value within the format's largest.
+// Scale byte 127 - bias from the bits of a block's max |x| in 32 bits. The
+// sum carries into the exponent exactly if the significand is above 1.75;
+// an amax below the normal range gives the largest bias, 126 (byte 1), by
+// itself. 0, infinity and NaN: bias 0.
 template <int FMT>
-__device__ inline uint32_t code4(float f0, float f1, float f2, float f3, float scale, bool odd) {
-  f0 *= scale;
-  f1 *= scale;
-  f2 *= scale;
-  f3 *= scale;
-  if (odd) {
-    constexpr float kMax = FMT == FP8_E4M3 ? 448.0f : 57344.0f;
-    f0 = f0 != f0 ? f0 : fminf(fmaxf(f0, -kMax), kMax);
-    f1 = f1 != f1 ? f1 : fminf(fmaxf(f1, -kMax), kMax);
-    f2 = f2 != f2 ? f2 : fminf(fmaxf(f2, -kMax), kMax);
-    f3 = f3 != f3 ? f3 : fminf(fmaxf(f3, -kMax), kMax);
-  }
-  int r;
-  if constexpr (FMT == FP8_E4M3) {
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(f0, f1, 0, false);
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(f2, f3, r, true);
-  } else {
-    r = __builtin_amdgcn_cvt_pk_bf8_f32(f0, f1, 0, false);
-    r = __builtin_amdgcn_cvt_pk_bf8_f32(f2, f3, r, true);
-  }
-  return (uint32_t)r;
+__device__ inline uint32_t scale_byte(uint32_t mag) {
+  constexpr int kTop = FMT == FP8_E4M3 ? kTopExpE4M3 : kTopExpE5M2;
+  const int e = (int)((mag + 0x1FFFFFu) >> 23) - kTop;
+  return mag - 1u < 0x7F7FFFFFu ? (uint32_t)(e > 1 ? e : 1) : 127u;
+}
+// 2^(byte - 127); bytes are 1 .. 253
+__device__ inline float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+template <int FMT, bool HI>
+__device__ inline uint32_t code2(uint32_t old, uint32_t pair, float scale) {  // two bf16
+  const bq_s16x2 o = __builtin_bit_cast(bq_s16x2, old);
+  const bq_bf16x2 v = __builtin_bit_cast(bq_bf16x2, pair);
+  if constexpr (FMT == FP8_E4M3)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, v, scale, HI));
+  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(o, v, scale, HI));
+}
+template <int FMT, bool HI>
+__device__ inline uint32_t code2(uint32_t old, float a, float b, float scale) {
+  const bq_s16x2 o = __builtin_bit_cast(bq_s16x2, old);
+  if constexpr (FMT == FP8_E4M3)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, a, b, scale, HI));
+  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(o, a, b, scale, HI));
+}
+template <int FMT>
+__device__ inline uint32_t code4(uint32_t p0, uint32_t p1, float s) {
+  return code2<FMT, true>(code2<FMT, false>(0, p0, s), p1, s);
+}
+template <int FMT>
+__device__ inline uint32_t code4(float a, float b, float c, float d, float s) {
+  return code2<FMT, true>(code2<FMT, false>(0, a, b, s), c, d, s);
+}
+
+// A block with an infinity or a NaN has scale 1: its values are clamped to
+// the format's largest, a NaN stays one. Such blocks are rare: callers
+// branch round this for a whole wave.
+template <int FMT>
+__device__ inline uint32_t clamp_pair(uint32_t pair, bool odd) {
+  constexpr uint32_t kMax = FMT == FP8_E4M3 ? 0x43E0u : 0x4760u;  // 448, 57344 in bf16
+  const uint32_t m = pair & 0x7FFF7FFFu;
+  uint32_t r = pk_min(m, kMax | kMax << 16);
+  if ((m & 0xFFFFu) > 0x7F80u) r |= 0x7FFFu;
+  if ((m >> 16) > 0x7F80u) r |= 0x7FFF0000u;
+  return odd ? r | (pair & 0x80008000u) : pair;
+}
+template <int FMT>
+__device__ inline float clamp_one(float f, bool odd) {
+  constexpr float kMax = FMT == FP8_E4M3 ? 448.0f : 57344.0f;
+  return !odd || f != f ? f : fminf(fmaxf(f, -kMax), kMax);
 }
 
 // 8 bf16 (four dwords) to 32 bits
@@ -63,14 +112,52 @@ __device__ inline void widen8(bq_u32x4 w, float f[8]) {
   }
 }
 
-// columns cx .. cx + 7 of a row, zeros past cols; in-bounds for any pitch
-__device__ inline bq_u32x4 load8(const uint16_t* row, int64_t cx, int64_t cols) {
-  if (cx + 8 <= cols) return __builtin_nontemporal_load((const bq_u32x4_a2*)(row + cx));
-  bq_u32x4 w = {0, 0, 0, 0};
+// Rows r, r + STEP, ... (N of them), columns cx .. cx + 7, of a matrix;
+// zeros past its ends; in-bounds for any pitch. `inside` (the same for the
+// whole workgroup): all of it exists. Otherwise each load is of the nearest
+// 8 columns and row that do exist, shifted and masked after all are issued;
+// matrices of fewer than 8 columns are gathered.
+template <int N, int STEP>
+__device__ inline void load_rows(const Bf16Mat& x, int64_t r, int64_t cx, bool inside, bq_u32x4 (&w)[N]) {
+  if (inside) {
+    const uint16_t* p = x.p + r * x.ld + cx;
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (cx + k < cols) w[k >> 1] |= (uint32_t)row[cx + k] << (16 * (k & 1));
-  return w;
+    for (int i = 0; i < N; ++i) w[i] = __builtin_nontemporal_load((const bq_u32x4_a2*)(p + i * STEP * x.ld));
+    return;
+  }
+  if (x.cols < 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = (bq_u32x4){0, 0, 0, 0};
+#pragma clang loop unroll(disable)
+    for (int k = 0; k < x.cols; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (r + i * STEP < x.rows && cx == 0) {
+          const uint32_t e = (uint32_t)x.p[(r + i * STEP) * x.ld + k] << (16 * (k & 1));
+          w[i].x |= k >> 1 == 0 ? e : 0;
+          w[i].y |= k >> 1 == 1 ? e : 0;
+          w[i].z |= k >> 1 == 2 ? e : 0;
+          w[i].w |= k >> 1 == 3 ? e : 0;
+        }
+    return;
+  }
+  const int64_t c = cx + 8 <= x.cols ? cx : x.cols - 8;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t q = r + i * STEP < x.rows ? r + i * STEP : x.rows - 1;
+    w[i] = *(const bq_u32x4_a2*)(x.p + q * x.ld + c);
+  }
+  const int sh = 16 * (int)(cx - c);  // bits of 128 that belong to earlier columns
+  const bool far = sh >= 64;
+  const int s = sh & 63;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool none = r + i * STEP >= x.rows || sh >= 128;
+    const uint64_t lo = (uint64_t)w[i].y << 32 | w[i].x, hi = (uint64_t)w[i].w << 32 | w[i].z;
+    const uint64_t l = far ? hi >> s : lo >> s | (hi << 1) << (63 - s), h = far ? 0 : hi >> s;
+    w[i] = (bq_u32x4){(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    if (none) w[i] = (bq_u32x4){0, 0, 0, 0};
+  }
 }
 
 __device__ inline uint32_t pack_bf16(float a, float b) {  // round to nearest even
@@ -78,119 +165,180 @@ __device__ inline uint32_t pack_bf16(float a, float b) {  // round to nearest ev
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bq_bf16x2));
 }
 
-__device__ inline void store8(uint16_t* row, int64_t cx, int64_t cols, const float f[8]) {
-  const bq_u32x4 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+__device__ inline void store8(uint16_t* row, int64_t cx, int64_t cols, bq_u32x4 w) {
   if (cx + 8 <= cols) {
     __builtin_nontemporal_store(w, (bq_u32x4_a2*)(row + cx));
     return;
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (cx + k < cols) row[cx + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+  const int n = (int)(cols - cx);  // below 8, or none
+  uint16_t* p = row + cx;
+  if (n <= 0) return;
+  if (n & 4) {
+    *(bq_u32x2_a2*)p = (bq_u32x2){w.x, w.y};
+    p += 4;
+    w.x = w.z;
+    w.y = w.w;
+  }
+  if (n & 2) {
+    *(bq_u32_a2*)p = w.x;
+    p += 2;
+    w.x = w.y;
+  }
+  if (n & 1) *p = (uint16_t)w.x;
+}
+__device__ inline bq_u32x4 pack8(const float f[8]) {
+  return (bq_u32x4){pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
 }
 
-// one row's 8 values in each of 16 lanes -> codes and scale byte of that
-// row's block (column cx = this lane's first; a whole block is written, so
-// columns past cols hold zero codes). All 16 lanes call it.
+// bits of the largest |x| of a row's block from 16 lanes' 8 values each
+__device__ inline uint32_t row_mag(const float f[8]) {
+  const float m = nan_max(nan_max(nan_max(f[0], f[1]), nan_max(f[2], f[3])),
+                          nan_max(nan_max(f[4], f[5]), nan_max(f[6], f[7])));
+  return row16_max(__float_as_uint(m) & 0x7FFFFFFFu);
+}
+__device__ inline uint32_t row_mag(bq_u32x4 w) {
+  const bq_u32x4 a = w & 0x7FFF7FFFu;
+  const uint32_t m = pk_max(pk_max(a.x, a.y), pk_max(a.z, a.w));
+  return row16_max(umax(m & 0xFFFFu, m >> 16)) << 16;
+}
+// one lane's 8 values of a row, 16 lanes to a block
+struct Row8 {
+  float f[8];
+};
 template <int FMT>
-__device__ inline void quant_row8(const float f[8], const BlockMat& o, int64_t row, int64_t cx) {
-  uint32_t m = 0;
+__device__ inline uint2 row_code(const Row8& v, float s) {
+  return make_uint2(code4<FMT>(v.f[0], v.f[1], v.f[2], v.f[3], s), code4<FMT>(v.f[4], v.f[5], v.f[6], v.f[7], s));
+}
+template <int FMT>
+__device__ inline uint2 row_code(bq_u32x4 w, float s) {
+  return make_uint2(code4<FMT>(w.x, w.y, s), code4<FMT>(w.z, w.w, s));
+}
+template <int FMT>
+__device__ inline Row8 clamp_row(Row8 v, bool odd) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = umax(m, mag_bits(f[k]));
-  m = row16_max(m);
-  const int32_t b = bias_from_amax_bits(m, FMT, 0, 0, nullptr);
-  const float s = pow2f(b);
-  const bool odd = m >= 0x7F800000u;
-  const uint2 q = make_uint2(code4<FMT>(f[0], f[1], f[2], f[3], s, odd), code4<FMT>(f[4], f[5], f[6], f[7], s, odd));
-  if (row < o.rows) {
-    *(uint2*)(o.codes + row * o.pitch + cx) = q;
-    if ((threadIdx.x & 15) == 0) o.scales[cx / kBlk * o.srows + scale_pos(row)] = (uint8_t)(127 - b);
+  for (int k = 0; k < 8; ++k) v.f[k] = clamp_one<FMT>(v.f[k], odd);
+  return v;
+}
+template <int FMT>
+__device__ inline bq_u32x4 clamp_row(bq_u32x4 w, bool odd) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = clamp_pair<FMT>(w[k], odd);
+  return w;
+}
+__device__ inline uint32_t row_mag(const Row8& v) { return row_mag(v.f); }
+
+// codes and scale bytes of N rows; one branch for all of them, so that
+// their reductions over lanes overlap
+template <int FMT, int N, typename V>
+__device__ inline void rows_codes(const V (&v)[N], uint2 (&q)[N], uint32_t (&byte)[N]) {
+  uint32_t m[N], all = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    m[i] = row_mag(v[i]);
+    all = umax(all, m[i]);
+    byte[i] = scale_byte<FMT>(m[i]);
+    q[i] = row_code<FMT>(v[i], scale_value(byte[i]));
+  }
+  if (__builtin_expect(__any(all >= 0x7F800000u), 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      q[i] = row_code<FMT>(clamp_row<FMT>(v[i], m[i] >= 0x7F800000u), scale_value(byte[i]));
   }
 }
 
-// codes of a row's 8 columns to 32 bits
+// Stores of rows that may not exist: through a buffer resource that ends
+// with the matrix's last row within the tile, so that a row past it is
+// dropped without a branch.
+__device__ inline __amdgpu_buffer_rsrc_t tile_rsrc(const BlockMat& o, int64_t r0, int rows) {
+  const int64_t n = o.rows - r0 < rows ? o.rows - r0 : rows;
+  return __builtin_amdgcn_make_buffer_rsrc(o.codes + r0 * o.pitch, (short)0, (int)(n * o.pitch), 0x00020000);
+}
+__device__ inline void put_codes(__amdgpu_buffer_rsrc_t r, uint2 q, int off) {
+  __builtin_amdgcn_raw_buffer_store_b64((bq_u32x2){q.x, q.y}, r, off, 0, 0);
+}
+// a row's scale byte (column cx: any of the block's)
+__device__ inline void put_byte(const BlockMat& o, int64_t row, int64_t cx, uint32_t byte) {
+  if ((threadIdx.x & 15) == 0 && row < o.rows) o.scales[cx / kBlk * o.srows + scale_pos(row)] = (uint8_t)byte;
+}
+
+// codes of a row's 8 columns to 32 bits: code * scale, exactly
 template <int FMT>
 __device__ inline void uncode8(uint2 q, float s, float f[8]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int w = (int)(k ? q.y : q.x);
+    const uint32_t w = k ? q.y : q.x;
     bq_f32x2 lo, hi;
     if constexpr (FMT == FP8_E4M3) {
-      lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-      hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+      lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
     } else {
-      lo = __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-      hi = __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
+      lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, s, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, s, true);
     }
-    f[4 * k] = lo.x * s;
-    f[4 * k + 1] = lo.y * s;
-    f[4 * k + 2] = hi.x * s;
-    f[4 * k + 3] = hi.y * s;
+    f[4 * k] = lo.x;
+    f[4 * k + 1] = lo.y;
+    f[4 * k + 2] = hi.x;
+    f[4 * k + 3] = hi.y;
   }
 }
-
-// 2^(byte - 127); bytes are 1 .. 253
-__device__ inline float scale_value(uint8_t byte) { return __uint_as_float((uint32_t)byte << 23); }
-
+// the same rounded to bf16 (exact but for values below its normal range)
 template <int FMT>
-__device__ inline void load_row8(const BlockMat& q, int64_t row, int64_t cx, float f[8]) {
-  const uint2 w = *(const uint2*)(q.codes + row * q.pitch + cx);
-  uncode8<FMT>(w, scale_value(q.scales[cx / kBlk * q.srows + scale_pos(row)]), f);
+__device__ inline bq_u32x4 uncode8_bf16(uint2 q, float s) {
+  bq_u32x4 r;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w = k ? q.y : q.x;
+    if constexpr (FMT == FP8_E4M3) {
+      r[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+      r[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true));
+    } else {
+      r[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, s, false));
+      r[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, s, true));
+    }
+  }
+  return r;
 }
 
-// LDS of the transposing part: the tile's codes and the column maxima of each wave
-struct QuantLds {
-  uint4 tile[kBlk * kBlk / 16];
-  uint32_t cmax[4][kBlk];
-};
+__device__ inline uint2 row_codes_at(const BlockMat& q, int64_t row, int64_t cx) {
+  return *(const uint2*)(q.codes + row * q.pitch + cx);
+}
+__device__ inline float row_scale_at(const BlockMat& q, int64_t row, int64_t cx) {
+  return scale_value(q.scales[cx / kBlk * q.srows + scale_pos(row)]);
+}
 
-// A tile in patches -> the transposed form: row trow0 + c0 + j of o holds
-// column c0 + j, its columns r0 .. r0 + 127 (o.rows: how many columns the
-// source has from c0 = 0 on; rows past the source's are zeros in v). The
-// whole workgroup calls it; a barrier at entry lets it follow itself.
-template <int FMT>
-__device__ inline void quant_cols(const float v[8][8], const BlockMat& o, int64_t trow0, int64_t r0, int64_t c0,
-                                  QuantLds& lds) {
-  const int t = threadIdx.x, rg = t >> 4, cc = t & 15;
-  uint32_t m[8];
+// ---- the transposing part ------------------------------------------------
+// A 128 x 128 tile's codes in LDS, 128 bytes a column of the source. A write
+// is a few rows of columns 8 cc + j for 16 cc, a read whole columns: odd
+// groups of 8 columns swap the two halves of each 256-byte bank line, and
+// 16-byte chunks are swizzled by pairs of groups, so that neither conflicts.
+__device__ inline int lds_chunk(int c, int chunk) { return (c ^ ((c >> 3) & 1)) * 8 + (chunk ^ ((c >> 4) & 7)); }
+
+// the tile to memory: row trow0 + c of o gets LDS column c, c < cols
+template <int THREADS>
+__device__ inline void put_tile(const uint4* tile, const BlockMat& o, int64_t trow0, int64_t cols, int64_t r0) {
+  const int n = (int)(cols < kBlk ? cols : kBlk);
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(o.codes + trow0 * o.pitch + r0, (short)0, (int)(n * o.pitch - r0), 0x00020000);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[j] = umax(m[j], mag_bits(v[i][j]));
-    m[j] = umax(m[j], (uint32_t)__shfl_xor((int)m[j], 16, 64));
-    m[j] = umax(m[j], (uint32_t)__shfl_xor((int)m[j], 32, 64));
-  }
-  __syncthreads();  // the tile and maxima of an earlier call are read
-  if ((t & 63) < 16) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) lds.cmax[t >> 6][8 * cc + j] = m[j];
-  }
-  __syncthreads();
-  uint8_t* const l8 = (uint8_t*)lds.tile;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = 8 * cc + j;
-    const uint32_t mm = umax(umax(lds.cmax[0][c], lds.cmax[1][c]), umax(lds.cmax[2][c], lds.cmax[3][c]));
-    const int32_t b = bias_from_amax_bits(mm, FMT, 0, 0, nullptr);
-    const float s = pow2f(b);
-    const bool odd = mm >= 0x7F800000u;
-    // 16-byte chunks of an LDS row are swizzled by (row / 8), which spreads
-    // the 8-byte writes over the banks
-    *(uint2*)(l8 + c * kBlk + ((((rg >> 1) ^ (cc & 7))) << 4) + 8 * (rg & 1)) =
-        make_uint2(code4<FMT>(v[0][j], v[1][j], v[2][j], v[3][j], s, odd),
-                   code4<FMT>(v[4][j], v[5][j], v[6][j], v[7][j], s, odd));
-    if (rg == 0 && c0 + c < o.rows)
-      o.scales[r0 / kBlk * o.srows + scale_pos(trow0 + c0 + c)] = (uint8_t)(127 - b);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int q = t + 256 * k;
+  for (int k = 0; k < 1024 / THREADS; ++k) {
+    const int q = threadIdx.x + THREADS * k;
     const int c = q >> 3, part = q & 7;
-    if (c0 + c < o.rows)
-      *(uint4*)(o.codes + (trow0 + c0 + c) * o.pitch + r0 + 16 * part) = lds.tile[c * 8 + (part ^ ((c >> 3) & 7))];
+    const uint4 v = tile[lds_chunk(c, part)];
+    __builtin_amdgcn_raw_buffer_store_b128((bq_u32x4){v.x, v.y, v.z, v.w}, r, c * (int)o.pitch + 16 * part, 0, 0);
   }
+}
+
+// Two values' maxima over pairs of lanes 32 (16) apart at once: the result
+// holds a's in the lower half (even rows of 16) and b's in the upper (odd).
+template <typename Max>
+__device__ inline uint32_t swap32_max(uint32_t a, uint32_t b, Max mx) {
+  const bq_u32x2 r = __builtin_bit_cast(bq_u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+  return mx(r.x, r.y);
+}
+template <typename Max>
+__device__ inline uint32_t swap16_max(uint32_t a, uint32_t b, Max mx) {
+  const bq_u32x2 r = __builtin_bit_cast(bq_u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+  return mx(r.x, r.y);
 }
 
 }  // namespace fp8lin

@@ -10,28 +10,82 @@
 namespace fp8lin {
 namespace {
 
-// 128 x 128 tile per workgroup: transposed form, and the row form if ROW
+// 128 x 128 tile per workgroup: transposed form, and the row form if ROW.
+// Thread t has rows 8 (t / 16) .. + 7, columns 8 (t % 16) .. + 7 as packed
+// bf16 (32 registers), so a row's block lies in 16 neighbouring lanes and a
+// column's in 16 lane groups of all four waves: its maximum is reduced
+// within a wave, then over LDS by one thread a column.
 template <int FMT, bool ROW>
 __global__ __launch_bounds__(256) void block_quant_tile_kernel(Bf16Mat x, BlockMat row, BlockMat tr, int64_t t_row0,
                                                                int tiles_c) {
-  __shared__ QuantLds lds;
+  __shared__ uint4 tile[kBlk * kBlk / 16];
+  __shared__ uint32_t cmax[4][kBlk / 2];  // of each wave, two columns' bf16 magnitudes a dword
+  __shared__ float cscale[kBlk];
+  __shared__ uint8_t rbyte[kBlk];         // in the scales' order
   const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * kBlk, c0 = (int64_t)(blockIdx.x % tiles_c) * kBlk;
   const int t = threadIdx.x, rg = t >> 4, cc = t & 15;
   const int64_t rr = r0 + 8 * rg, cx = c0 + 8 * cc;
   bq_u32x4 w[8];
+  load_rows<8, 1>(x, rr, cx, r0 + kBlk <= x.rows && c0 + kBlk <= x.cols, w);
+  bq_u32x4 cm = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    w[i] = (bq_u32x4){0, 0, 0, 0};
-    if (rr + i < x.rows) w[i] = load8(x.p + (rr + i) * x.ld, cx, x.cols);
-  }
-  float v[8][8];
+    const bq_u32x4 a = w[i] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) widen8(w[i], v[i]);
+    for (int d = 0; d < 4; ++d) cm[d] = pk_max(cm[d], a[d]);
+  }
   if constexpr (ROW) {
+    uint2 q[8];
+    uint32_t byte[8];
+    rows_codes<FMT>(w, q, byte);
+    const __amdgpu_buffer_rsrc_t r = tile_rsrc(row, r0, kBlk);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) quant_row8<FMT>(v[i], row, rr + i, cx);
+    for (int i = 0; i < 8; ++i) {
+      put_codes(r, q[i], (8 * rg + i) * (int)row.pitch + (int)cx);
+      if (cc == 0) rbyte[(8 * (rg & 1) + i) * 8 + (rg >> 1)] = (uint8_t)byte[i];
+    }
   }
-  quant_cols<FMT>(v, tr, t_row0, r0, c0, lds);
+  // dword R of the four in the R-th 16 lanes
+  cmax[t >> 6][4 * cc + (rg & 3)] =
+      swap16_max(swap32_max(cm[0], cm[2], pk_max), swap32_max(cm[1], cm[3], pk_max), pk_max);
+  __syncthreads();
+  if (t < kBlk) {
+    const int sh = 16 * (t & 1);
+    const uint32_t m =
+        pk_max(pk_max(cmax[0][t >> 1], cmax[1][t >> 1]), pk_max(cmax[2][t >> 1], cmax[3][t >> 1])) >> sh << 16;
+    const uint32_t byte = scale_byte<FMT>(m);
+    cscale[t] = m < 0x7F800000u ? scale_value(byte) : -1.0f;
+    if (c0 + t < tr.rows) tr.scales[r0 / kBlk * tr.srows + scale_pos(t_row0 + c0 + t)] = (uint8_t)byte;
+  } else if (ROW) {
+    const int p = t - kBlk;
+    if (r0 + 16 * (p & 7) + (p >> 3) < row.rows) row.scales[c0 / kBlk * row.srows + r0 + p] = rbyte[p];
+  }
+  __syncthreads();
+  float s[8];  // negative: an infinity or a NaN in the column
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s[j] = cscale[8 * cc + j];
+    odd |= s[j] < 0;
+  }
+  odd = __builtin_expect(__any(odd), 0);
+  uint8_t* const l8 = (uint8_t*)tile;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t p[4];  // rows 2 k, 2 k + 1 of column j
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      p[k] = __builtin_amdgcn_perm(w[2 * k + 1][j >> 1], w[2 * k][j >> 1], j & 1 ? 0x07060302 : 0x05040100);
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = clamp_pair<FMT>(p[k], s[j] < 0);
+      s[j] = __builtin_fabsf(s[j]);
+    }
+    *(uint2*)(l8 + 16 * lds_chunk(8 * cc + j, rg >> 1) + 8 * (rg & 1)) =
+        make_uint2(code4<FMT>(p[0], p[1], s[j]), code4<FMT>(p[2], p[3], s[j]));
+  }
+  __syncthreads();
+  put_tile<256>(tile, tr, t_row0 + c0, tr.rows - c0, r0);
 }
 
 // row form only: 16 RPT rows x 128 columns per workgroup
@@ -41,16 +95,15 @@ __global__ __launch_bounds__(256) void block_quant_rows_kernel(Bf16Mat x, BlockM
   const int t = threadIdx.x;
   const int64_t rr = r0 + (t >> 4), cx = c0 + 8 * (t & 15);
   bq_u32x4 w[RPT];
+  load_rows<RPT, 16>(x, rr, cx, r0 + 16 * RPT <= x.rows && c0 + kBlk <= x.cols, w);
+  uint2 q[RPT];
+  uint32_t byte[RPT];
+  rows_codes<FMT>(w, q, byte);
+  const __amdgpu_buffer_rsrc_t r = tile_rsrc(row, r0, 16 * RPT);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    w[i] = (bq_u32x4){0, 0, 0, 0};
-    if (rr + 16 * i < x.rows) w[i] = load8(x.p + (rr + 16 * i) * x.ld, cx, x.cols);
-  }
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    float f[8];
-    widen8(w[i], f);
-    quant_row8<FMT>(f, row, rr + 16 * i, cx);
+    put_codes(r, q[i], ((t >> 4) + 16 * i) * (int)row.pitch + (int)cx);
+    put_byte(row, rr + 16 * i, cx, byte[i]);
   }
 }
 
@@ -60,13 +113,20 @@ __global__ __launch_bounds__(256) void block_dequant_kernel(BlockMat q, uint16_t
   const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * (16 * RPT), c0 = (int64_t)(blockIdx.x % tiles_c) * kBlk;
   const int t = threadIdx.x;
   const int64_t rr = r0 + (t >> 4), cx = c0 + 8 * (t & 15);
-  float f[RPT][8];
+  uint2 c[RPT];
+  float s[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    c[i] = make_uint2(0, 0);
+    s[i] = 1.0f;
+    if (rr + 16 * i < q.rows) {
+      c[i] = row_codes_at(q, rr + 16 * i, cx);
+      s[i] = row_scale_at(q, rr + 16 * i, cx);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    if (rr + 16 * i < q.rows) load_row8<FMT>(q, rr + 16 * i, cx, f[i]);
-#pragma unroll
-  for (int i = 0; i < RPT; ++i)
-    if (rr + 16 * i < q.rows) store8(out + (rr + 16 * i) * ld, cx, q.cols, f[i]);
+    if (rr + 16 * i < q.rows) store8(out + (rr + 16 * i) * ld, cx, q.cols, uncode8_bf16<FMT>(c[i], s[i]));
 }
 
 // rows a thread takes in the row kernels: 8 keeps many loads in flight, 1

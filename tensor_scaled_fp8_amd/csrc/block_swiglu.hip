@@ -22,7 +22,7 @@ struct Grads {
 __device__ inline Grads grads(float g, float u, float dh) {
   const float s = sigmoid(g);
   const float gs = g * s;
-  return {dh * u * s * (1.0f + g * (1.0f - s)), dh * gs, gs * u};
+  return {dh * u * __builtin_fmaf(gs, 1.0f - s, s), dh * gs, gs * u};
 }
 
 template <int RPT>
@@ -32,28 +32,34 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(Bf16Mat gate, Bf16Mat u
   const int t = threadIdx.x;
   const int64_t rr = r0 + (t >> 4), cx = c0 + 8 * (t & 15);
   bq_u32x4 wg[RPT], wu[RPT];
+  const bool inside = r0 + 16 * RPT <= gate.rows && c0 + kBlk <= gate.cols;
+  load_rows<RPT, 16>(gate, rr, cx, inside, wg);
+  load_rows<RPT, 16>(up, rr, cx, inside, wu);
+  Row8 y[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    wg[i] = wu[i] = (bq_u32x4){0, 0, 0, 0};
-    if (rr + 16 * i < gate.rows) {
-      wg[i] = load8(gate.p + (rr + 16 * i) * gate.ld, cx, gate.cols);
-      wu[i] = load8(up.p + (rr + 16 * i) * up.ld, cx, gate.cols);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int64_t r = rr + 16 * i;
-    float g[8], u[8], y[8];
+    float g[8], u[8];
     widen8(wg[i], g);
     widen8(wu[i], u);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = g[k] * sigmoid(g[k]) * u[k];
-    if (h && r < gate.rows) store8(h + r * ldh, cx, gate.cols, y);
-    if (hq.codes) quant_row8<FP8_E4M3>(y, hq, r, cx);
-    if (gq.codes) {
-      quant_row8<FP8_E4M3>(g, gq, r, cx);
-      quant_row8<FP8_E4M3>(u, uq, r, cx);
+    for (int k = 0; k < 8; ++k) y[i].f[k] = g[k] * sigmoid(g[k]) * u[k];
+    if (h && rr + 16 * i < gate.rows) store8(h + (rr + 16 * i) * ldh, cx, gate.cols, pack8(y[i].f));
+  }
+  auto put = [&](const BlockMat& o, const auto& v) {
+    uint2 q[RPT];
+    uint32_t byte[RPT];
+    rows_codes<FP8_E4M3>(v, q, byte);
+    const __amdgpu_buffer_rsrc_t r = tile_rsrc(o, r0, 16 * RPT);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      put_codes(r, q[i], ((t >> 4) + 16 * i) * (int)o.pitch + (int)cx);
+      put_byte(o, rr + 16 * i, cx, byte[i]);
     }
+  };
+  if (hq.codes) put(hq, y);
+  if (gq.codes) {
+    put(gq, wg);
+    put(uq, wu);
   }
 }
 
@@ -64,89 +70,166 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(Bf16Mat dh, BlockMat gq
   const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * (16 * RPT), c0 = (int64_t)(blockIdx.x % tiles_c) * kBlk;
   const int t = threadIdx.x;
   const int64_t rr = r0 + (t >> 4), cx = c0 + 8 * (t & 15);
+  bq_u32x4 wd[RPT];
+  uint2 wg[RPT], wu[RPT];
+  float sg[RPT], su[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int64_t r = rr + 16 * i;
+    wg[i] = wu[i] = make_uint2(0, 0);
+    sg[i] = su[i] = 1.0f;
+    if (r < dh.rows) {
+      wg[i] = row_codes_at(gq, r, cx);
+      wu[i] = row_codes_at(uq, r, cx);
+      sg[i] = row_scale_at(gq, r, cx);
+      su[i] = row_scale_at(uq, r, cx);
+    }
+  }
+  load_rows<RPT, 16>(dh, rr, cx, r0 + 16 * RPT <= dh.rows && c0 + kBlk <= dh.cols, wd);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int64_t r = rr + 16 * i;
     if (r >= dh.rows) continue;
     float g[8], u[8], d[8], a[8], b[8];
-    widen8(load8(dh.p + r * dh.ld, cx, dh.cols), d);
-    load_row8<FP8_E4M3>(gq, r, cx, g);
-    load_row8<FP8_E4M3>(uq, r, cx, u);
+    widen8(wd[i], d);
+    uncode8<FP8_E4M3>(wg[i], sg[i], g);
+    uncode8<FP8_E4M3>(wu[i], su[i], u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const Grads x = grads(g[k], u[k], d[k]);
       a[k] = x.dg;
       b[k] = x.du;
     }
-    if (dg) store8(dg + r * lddg, cx, dh.cols, a);
-    if (du) store8(du + r * lddu, cx, dh.cols, b);
+    if (dg) store8(dg + r * lddg, cx, dh.cols, pack8(a));
+    if (du) store8(du + r * lddu, cx, dh.cols, pack8(b));
   }
 }
 
-// One 128 x 128 tile: the E5M2 row and transposed forms of dg and du, and
-// the E4M3 transposed form of h'. The three are made one after the other
-// from the same loaded operands, so 64 results are live at a time. dh.p
-// null: h' only.
-__global__ __launch_bounds__(256) void swiglu_bwd_quant_kernel(Bf16Mat dh, BlockMat gq, BlockMat uq, BlockMat dgq,
-                                                               BlockMat duq, BlockMat dgut, BlockMat ht, int tiles_c) {
-  __shared__ QuantLds lds;
+// One 128 x 128 tile: the E5M2 row and transposed forms of dg and du and
+// the E4M3 transposed form of h', all from one evaluation: a thread of 512
+// holds the three at 4 rows x 8 columns in 32 bits (96 of 172 registers, two
+// waves a SIMD; held to 128 registers it spilled, 57 -> 108 us) until the
+// columns' maxima are known. dh.p null: h' only.
+__device__ inline uint32_t bits_max(uint32_t a, uint32_t b) {
+  return __float_as_uint(nan_max(__uint_as_float(a), __uint_as_float(b)));
+}
+__global__ __launch_bounds__(512) void swiglu_bwd_quant_kernel(Bf16Mat dh, BlockMat gq, BlockMat uq, BlockMat dgq,
+                                                                  BlockMat duq, BlockMat dgut, BlockMat ht,
+                                                                  int tiles_c) {
+  __shared__ uint4 tile[3][kBlk * kBlk / 16];  // h', dg, du
+  __shared__ float cmax[3][8][kBlk];           // of each wave
+  __shared__ float cscale[3][kBlk];
   const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * kBlk, c0 = (int64_t)(blockIdx.x % tiles_c) * kBlk;
-  const int t = threadIdx.x, rg = t >> 4, cc = t & 15;
-  const int64_t rr = r0 + 8 * rg, cx = c0 + 8 * cc;
-  bq_u32x4 wd[8];
-  uint2 wg[8], wu[8];
-  float sg[8], su[8];
+  const int t = threadIdx.x, rg = t >> 4, cc = t & 15, wave = t >> 6;
+  const int64_t rr = r0 + 4 * rg, cx = c0 + 8 * cc;
+  const int64_t f = dh.cols;
+  bq_u32x4 wd[4];
+  uint2 wg[4], wu[4];
+  float sg[4], su[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = rr + i;
     wd[i] = (bq_u32x4){0, 0, 0, 0};
     wg[i] = wu[i] = make_uint2(0, 0);
-    sg[i] = su[i] = 0.0f;
-    const int64_t r = rr + i;
+    sg[i] = su[i] = 1.0f;
     if (r < dh.rows) {
-      if (dh.p) wd[i] = load8(dh.p + r * dh.ld, cx, dh.cols);
-      wg[i] = *(const uint2*)(gq.codes + r * gq.pitch + cx);
-      wu[i] = *(const uint2*)(uq.codes + r * uq.pitch + cx);
-      sg[i] = scale_value(gq.scales[cx / kBlk * gq.srows + scale_pos(r)]);
-      su[i] = scale_value(uq.scales[cx / kBlk * uq.srows + scale_pos(r)]);
+      wg[i] = row_codes_at(gq, r, cx);
+      wu[i] = row_codes_at(uq, r, cx);
+      sg[i] = row_scale_at(gq, r, cx);
+      su[i] = row_scale_at(uq, r, cx);
     }
   }
-  const int64_t f = dh.cols;
-  float v[8][8];
-  auto fill = [&](auto pick) {
+  if (dh.p) load_rows<4, 1>(dh, rr, cx, r0 + kBlk <= dh.rows && c0 + kBlk <= f, wd);
+  Row8 v[3][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float d[8], g[8], u[8];
-      widen8(wd[i], d);
-      uncode8<FP8_E4M3>(wg[i], sg[i], g);
-      uncode8<FP8_E4M3>(wu[i], su[i], u);
+  for (int i = 0; i < 4; ++i) {
+    float d[8], g[8], u[8];
+    widen8(wd[i], d);
+    uncode8<FP8_E4M3>(wg[i], sg[i], g);
+    uncode8<FP8_E4M3>(wu[i], su[i], u);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = pick(grads(g[k], u[k], d[k]));
+    for (int k = 0; k < 8; ++k) {
+      const Grads x = grads(g[k], u[k], d[k]);
+      v[0][i].f[k] = x.h;
+      v[1][i].f[k] = x.dg;
+      v[2][i].f[k] = x.du;
     }
-  };
-  if (ht.codes) {
-    fill([](const Grads& x) { return x.h; });
-    quant_cols<FP8_E4M3>(v, ht, 0, r0, c0, lds);
   }
-  if (!dh.p) return;
-  fill([](const Grads& x) { return x.dg; });
   if (dgq.codes) {
+    auto put = [&](const BlockMat& o, const Row8 (&x)[4]) {
+      uint2 q[4];
+      uint32_t byte[4];
+      rows_codes<FP8_E5M2>(x, q, byte);
+      const __amdgpu_buffer_rsrc_t r = tile_rsrc(o, r0, kBlk);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) quant_row8<FP8_E5M2>(v[i], dgq, rr + i, cx);
+      for (int i = 0; i < 4; ++i) {
+        put_codes(r, q[i], (4 * rg + i) * (int)o.pitch + (int)cx);
+        put_byte(o, rr + i, cx, byte[i]);
+      }
+    };
+    put(dgq, v[1]);
+    put(duq, v[2]);
   }
-  if (dgut.codes) {
-    BlockMat o = dgut;
-    o.rows = f;  // dg's rows of the transposed form are 0 .. f - 1, du's f .. 2 f - 1
-    quant_cols<FP8_E5M2>(v, o, 0, r0, c0, lds);
-  }
-  fill([](const Grads& x) { return x.du; });
-  if (duq.codes) {
+  if (!dgut.codes && !ht.codes) return;
+  // columns 2 R, 2 R + 1 of the eight in the R-th 16 lanes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) quant_row8<FP8_E5M2>(v[i], duq, rr + i, cx);
+  for (int a = 0; a < 3; ++a) {
+    uint32_t m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      m[j] = __float_as_uint(nan_max(nan_max(v[a][0].f[j], v[a][1].f[j]), nan_max(v[a][2].f[j], v[a][3].f[j])));
+    float2 q;
+    uint32_t p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = swap32_max(m[j], m[j + 4], bits_max);
+    q.x = __uint_as_float(swap16_max(p[0], p[2], bits_max));
+    q.y = __uint_as_float(swap16_max(p[1], p[3], bits_max));
+    *(float2*)&cmax[a][wave][8 * cc + 2 * (rg & 3)] = q;
   }
+  __syncthreads();
+  if (t < 3 * kBlk) {
+    const int a = t >> 7, c = t & 127;
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = nan_max(m, cmax[a][k][c]);
+    const uint32_t mag = __float_as_uint(m) & 0x7FFFFFFFu;
+    const uint32_t byte = a == 0 ? scale_byte<FP8_E4M3>(mag) : scale_byte<FP8_E5M2>(mag);
+    cscale[a][c] = mag < 0x7F800000u ? scale_value(byte) : -1.0f;
+    const BlockMat& o = a == 0 ? ht : dgut;
+    // dg's rows of the transposed gradient are 0 .. f - 1, du's f .. 2 f - 1
+    if (o.codes && c0 + c < f) o.scales[r0 / kBlk * o.srows + scale_pos((a == 2 ? f : 0) + c0 + c)] = (uint8_t)byte;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 3; ++a) {
+    uint8_t* const l8 = (uint8_t*)tile[a];
+    float s[8];  // negative: an infinity or a NaN in the column
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[j] = cscale[a][8 * cc + j];
+      odd |= s[j] < 0;
+    }
+    odd = __builtin_expect(__any(odd), 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x[4] = {v[a][0].f[j], v[a][1].f[j], v[a][2].f[j], v[a][3].f[j]};
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = a == 0 ? clamp_one<FP8_E4M3>(x[i], s[j] < 0) : clamp_one<FP8_E5M2>(x[i], s[j] < 0);
+        s[j] = __builtin_fabsf(s[j]);
+      }
+      const uint32_t q = a == 0 ? code4<FP8_E4M3>(x[0], x[1], x[2], x[3], s[j])
+                                : code4<FP8_E5M2>(x[0], x[1], x[2], x[3], s[j]);
+      *(uint32_t*)(l8 + 16 * lds_chunk(8 * cc + j, rg >> 2) + 4 * (rg & 3)) = q;
+    }
+  }
+  __syncthreads();
+  if (ht.codes) put_tile<512>(tile[0], ht, c0, f - c0, r0);
   if (dgut.codes) {
-    BlockMat o = dgut;
-    o.rows = f;
-    quant_cols<FP8_E5M2>(v, o, f, r0, c0, lds);
+    put_tile<512>(tile[1], dgut, c0, f - c0, r0);
+    put_tile<512>(tile[2], dgut, f + c0, f - c0, r0);
   }
 }
 
@@ -184,7 +267,7 @@ hipError_t launch_swiglu_bwd_quant(const Bf16Mat& dh, const BlockMat& gq, const 
                                    const BlockMat& duq, const BlockMat& dgut, const BlockMat& ht, hipStream_t st) {
   if (dh.rows == 0 || dh.cols == 0) return hipSuccess;
   const int64_t tc = (dh.cols + kBlk - 1) / kBlk;
-  swiglu_bwd_quant_kernel<<<dim3((unsigned)((dh.rows + kBlk - 1) / kBlk * tc)), 256, 0, st>>>(dh, gq, uq, dgq, duq,
+  swiglu_bwd_quant_kernel<<<dim3((unsigned)((dh.rows + kBlk - 1) / kBlk * tc)), 512, 0, st>>>(dh, gq, uq, dgq, duq,
                                                                                             dgut, ht, (int)tc);
   return hipGetLastError();
 }
