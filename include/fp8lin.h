@@ -649,6 +649,15 @@ fp8_status fp8_block_linear_fwd_cached(const void* X_bf16, int64_t ldx, int64_t 
                                        size_t scratch_bytes, void* Y_bf16, hipStream_t stream);
 
 /*
+ * The same, by the same kernel, without scratch, where X is one row or a
+ * few: fp8_block_linear_few says whether it is for these sizes (1 or 0;
+ * M <= 16 and M * ceil(K / 128) <= 256), else FP8_ERR_UNSUPPORTED.
+ */
+int fp8_block_linear_few(int64_t M, int64_t K, int64_t N);
+fp8_status fp8_block_linear_fwd_few(const void* X_bf16, int64_t ldx, int64_t M, int64_t K, int64_t N,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, void* Y_bf16, hipStream_t stream);
+
+/*
  * SwiGLU: h = gate sigmoid(gate) up, all [rows, cols]. kept (or NULL)
  * receives the E4M3 block-scaled gate and up; the backward computes at
  * those: with g, u their values and s = sigmoid(g),

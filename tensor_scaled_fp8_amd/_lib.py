@@ -63,6 +63,8 @@ SIGNATURES = {
     "fp8_block_linear_bwd": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp, c_sz, c_vp, c_vp,
                                      c_vp]),
     "fp8_block_linear_cached_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "fp8_block_linear_few": (c_int, [c_i64, c_i64, c_i64]),
+    "fp8_block_linear_fwd_few": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]),
     "fp8_block_linear_fwd_cached": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
     "fp8_swiglu_kept_bytes": (c_sz, [c_i64, c_i64]),
     "fp8_swiglu_fwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]),

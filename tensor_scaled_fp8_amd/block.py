@@ -195,7 +195,8 @@ def _gemm_bytes(M: int, N: int, R: int) -> int:
 
 @functools.lru_cache(maxsize=4096)
 def _cached_bytes(M: int, K: int, N: int) -> int:
-    return load().fp8_block_linear_cached_bytes(M, K, N)
+    """Scratch of the serving linear; 0: the form for few rows, which takes none."""
+    return 0 if load().fp8_block_linear_few(M, K, N) else load().fp8_block_linear_cached_bytes(M, K, N)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -302,8 +303,11 @@ def fp8_block_linear_fwd_cached(X: torch.Tensor, w: BlockTensor, Y: Optional[tor
     elif tuple(Y.shape) != (M, N) or Y.dtype is not _BF16 or not Y.is_contiguous() or Y.device != X.device:
         raise ValueError("Y must be a contiguous bf16 [M, N] on X's device")
     nb = _cached_bytes(M, K, N)
-    scratch = _space(nb, X.device)
     c, s = w.pointers()
+    if not nb:
+        check(load().fp8_block_linear_fwd_few(p, ld, M, K, N, c, s, Y.data_ptr(), _on(X)), "fp8_block_linear_fwd_few")
+        return Y
+    scratch = _space(nb, X.device)
     check(load().fp8_block_linear_fwd_cached(p, ld, M, K, N, c, s, scratch.data_ptr(), nb, Y.data_ptr(), _on(X)),
           "fp8_block_linear_fwd_cached")
     return Y

@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(PKG, "lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8lin.so")
 SOURCES = ["api.hip", "amax.hip", "cast.hip", "gemm.hip", "adam.hip", "block_quant.hip", "block_swiglu.hip",
-           "block_gemm.hip", "block_api.hip"]
+           "block_gemm.hip", "block_serve.hip", "block_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

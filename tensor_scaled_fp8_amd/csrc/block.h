@@ -56,6 +56,18 @@ struct BlockGemm {
 size_t block_gemm_ws_bytes(int64_t M, int64_t N, int64_t R);
 hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipStream_t st);
 
+// Y [M, N] bf16 (dense) = X [M, K] W for few rows of X, W stored as w [N, K]
+// in E4M3. Fused: X is bf16 and of at most kServeBlocks blocks of 128 (two
+// rows of K = 8192: 20.1 us against 21.6 with X quantised by a launch of its
+// own, which is what more blocks cost). Otherwise X comes stored, of at most
+// 16 rows, or 32 where a workgroup has 16 columns or more to read it for (32
+// rows by 12288: 19.1 us; the tiled product 24).
+constexpr int64_t kServeBlocks = 256;
+bool block_serve_fused(int64_t M, int64_t K);
+bool block_serve_takes(int64_t M, int64_t N);
+hipError_t launch_block_serve_fused(const Bf16Mat& x, const BlockMat& w, uint16_t* y, hipStream_t st);
+hipError_t launch_block_serve(const BlockMat& xq, const BlockMat& w, uint16_t* y, hipStream_t st);
+
 // SwiGLU: h = g sigmoid(g) u. Outputs that are null are not written:
 // h bf16 [rows, cols]; hq its E4M3 form; gq, uq the E4M3 forms of g and u.
 hipError_t launch_swiglu_fwd(const Bf16Mat& gate, const Bf16Mat& up, uint16_t* h, int64_t ldh, const BlockMat& hq,

@@ -295,9 +295,26 @@ fp8_status fp8_block_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, in
   if (!bf16_ok(X, M, K, ldx) || !codes_ok(w_codes, w_scales, N, K) || !bf16_ok(Y, M, N, N)) return FP8_ERR_INVALID;
   const LinearFwd f(scratch, M, K, N, false);
   if (!space_ok(scratch, scratch_bytes, f.bytes)) return FP8_ERR_INVALID;
-  TRY(launch_block_quantize({(const uint16_t*)X, ldx, M, K}, FP8_E4M3, f.x, kNone, 0, stream));
-  return hip_status(launch_block_gemm({f.x, mat(w_codes, w_scales, N, K), FP8_E4M3, FP8_E4M3, (uint16_t*)Y, N}, f.part,
-                                      f.part_bytes, stream));
+  const Bf16Mat x = {(const uint16_t*)X, ldx, M, K};
+  const BlockMat w = mat(w_codes, w_scales, N, K);
+  if (block_serve_fused(M, K)) return hip_status(launch_block_serve_fused(x, w, (uint16_t*)Y, stream));
+  TRY(launch_block_quantize(x, FP8_E4M3, f.x, kNone, 0, stream));
+  if (block_serve_takes(M, N)) return hip_status(launch_block_serve(f.x, w, (uint16_t*)Y, stream));
+  return hip_status(launch_block_gemm({f.x, w, FP8_E4M3, FP8_E4M3, (uint16_t*)Y, N}, f.part, f.part_bytes, stream));
+}
+
+int fp8_block_linear_few(int64_t M, int64_t K, int64_t N) {
+  return linear_size(M, K, N) == FP8_OK && block_serve_fused(M, K);
+}
+
+fp8_status fp8_block_linear_fwd_few(const void* X, int64_t ldx, int64_t M, int64_t K, int64_t N, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, void* Y, hipStream_t stream) {
+  const fp8_status s = linear_size(M, K, N);
+  if (s != FP8_OK) return s;
+  if (!bf16_ok(X, M, K, ldx) || !codes_ok(w_codes, w_scales, N, K) || !bf16_ok(Y, M, N, N)) return FP8_ERR_INVALID;
+  if (!block_serve_fused(M, K)) return FP8_ERR_UNSUPPORTED;
+  return hip_status(launch_block_serve_fused({(const uint16_t*)X, ldx, M, K}, mat(w_codes, w_scales, N, K), (uint16_t*)Y,
+                                             stream));
 }
 
 size_t fp8_swiglu_kept_bytes(int64_t rows, int64_t cols) {

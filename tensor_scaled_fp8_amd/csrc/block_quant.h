@@ -116,13 +116,17 @@ __device__ inline void widen8(bq_u32x4 w, float f[8]) {
 // zeros past its ends; in-bounds for any pitch. `inside` (the same for the
 // whole workgroup): all of it exists. Otherwise each load is of the nearest
 // 8 columns and row that do exist, shifted and masked after all are issued;
-// matrices of fewer than 8 columns are gathered.
-template <int N, int STEP>
+// matrices of fewer than 8 columns are gathered. ONCE: nobody else reads it.
+template <int N, int STEP, bool ONCE = true>
 __device__ inline void load_rows(const Bf16Mat& x, int64_t r, int64_t cx, bool inside, bq_u32x4 (&w)[N]) {
   if (inside) {
     const uint16_t* p = x.p + r * x.ld + cx;
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __builtin_nontemporal_load((const bq_u32x4_a2*)(p + i * STEP * x.ld));
+    for (int i = 0; i < N; ++i) {
+      const bq_u32x4_a2* q = (const bq_u32x4_a2*)(p + i * STEP * x.ld);
+      if constexpr (ONCE) w[i] = __builtin_nontemporal_load(q);
+      else w[i] = *q;
+    }
     return;
   }
   if (x.cols < 8) {
