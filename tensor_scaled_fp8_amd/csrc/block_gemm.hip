@@ -8,12 +8,20 @@
 //
 // Both operands have one row per output index, 128-byte blocks along it.
 // A workgroup (4 waves, 2 x 2) makes a BM x BN tile: stages of one k-block
-// (BM + BN cache lines) are copied to LDS by buffer loads, kSlots - 1
-// stages ahead; the scales of a stage (one byte a row) go to registers. A
-// lane's offset past the operand's last row reads zeros, so tiles need no
-// bounds in the loop. With few tiles the reduction is split over several
-// workgroups, whose FP32 partial sums a second kernel adds in a fixed
-// order: results never depend on timing.
+// (BM + BN cache lines) are copied to LDS by buffer loads, SLOTS of them in
+// flight or in use; the scales of a stage (one byte a row) go to registers.
+// A wave reads a stage's fragments from LDS to registers during the MFMAs
+// of the stage before: read in their own stage, LDS and matrix pipes took
+// turns (a k-block of a 256 x 128 tile 1.07 us; this way 0.62). A lane's
+// offset past the operand's last row reads zeros, so tiles need no bounds in
+// the loop. With few tiles the reduction is split over several workgroups,
+// whose FP32 partial sums a second kernel adds in a fixed order: results
+// never depend on timing. Bound by the matrix pipes under the power limit
+// where the 256 x 256 tile fits (8192^3: 355 us, 3.1 PFLOP/s), by LDS and L2
+// reads a FLOP below it.
+// The instruction itself sums its 128 products to about 2^-16 of their
+// magnitude (FP32 partial sums measured against 64 bits: 1.5e-5 rms, no
+// bias); the length of the reduction adds nothing to that.
 #include <type_traits>
 
 #include "block.h"
@@ -178,22 +186,23 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
     const int row = 32 * i + 8 * w + (lane >> 3);
     offb[i] = row * (int)p.pb + 16 * ((lane & 7) ^ swz(row));
   }
-  // a stage past the last is loaded through a resource of no bytes, so that
-  // the count of loads in flight is the same in every step
-  auto issue = [&](int slot, int s) {
+  // load i of a stage, A's first; a stage past the last is loaded through a
+  // resource of no bytes, so that the count of loads in flight is the same
+  // in every step
+  auto issue = [&](int slot, int s, auto I_) {
+    constexpr int i = decltype(I_)::value;
     const int ko = s < nk ? s * kBlk : 0;
-    const __amdgpu_buffer_rsrc_t ra =
-        __builtin_amdgcn_make_buffer_rsrc((void*)abase, (short)0, s < nk ? abytes : 0, kRsrcWord3);
-    const __amdgpu_buffer_rsrc_t rb =
-        __builtin_amdgcn_make_buffer_rsrc((void*)bbase, (short)0, s < nk ? bbytes : 0, kRsrcWord3);
     lds_u8* d = l8 + slot * kStage + 1024 * w;
-#pragma unroll
-    for (int i = 0; i < LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void*)(d + 4096 * i), 16, offa[i], ko, 0, 0);
-    d += BM * kBlk;
-#pragma unroll
-    for (int i = 0; i < LB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void*)(d + 4096 * i), 16, offb[i], ko, 0, 0);
+    if constexpr (i < LA) {
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)abase, (short)0, s < nk ? abytes : 0, kRsrcWord3);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(d + 4096 * i), 16, offa[i], ko, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)bbase, (short)0, s < nk ? bbytes : 0, kRsrcWord3);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(d + BM * kBlk + 4096 * (i - LA)), 16, offb[i - LA], ko,
+                                               0, 0);
+    }
   };
 
   // scales of a stage: the wave's FM (FN) row blocks are FM consecutive
@@ -231,47 +240,64 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
 
   using FMc = std::integral_constant<int, FM>;
   using FNc = std::integral_constant<int, FN>;
-  u32x2 xa[SLOTS - 1], xb[SLOTS - 1];  // scales of the stages in flight
-  static_for<SLOTS - 1>([&](auto S_) {
-    constexpr int s = decltype(S_)::value;
-    xa[s] = scale_load(p.sa, asz, soffa, kblock(s) * (int)p.sra, FMc{});
-    xb[s] = scale_load(p.sb, bsz, soffb, kblock(s) * (int)p.srb, FNc{});
-    issue(s, s);
+  // fragments of stage s in [s % 2], scales in [s % RING]
+  constexpr int RING = SLOTS == 3 ? 3 : 4, UNROLL = SLOTS == 3 ? 6 : 4;
+  v8i fa[2][FM], fb[2][FN];
+  u32x2 xa[RING], xb[RING];
+  auto scales = [&](int s, auto R_) {
+    constexpr int r = decltype(R_)::value;
+    xa[r] = scale_load(p.sa, asz, soffa, kblock(s) * (int)p.sra, FMc{});
+    xb[r] = scale_load(p.sb, bsz, soffb, kblock(s) * (int)p.srb, FNc{});
+  };
+  // fragment r of a stage, B's first
+  auto read = [&](int slot, auto P_, auto R_) {
+    constexpr int par = decltype(P_)::value, r = decltype(R_)::value;
+    if constexpr (r < FN) fb[par][r] = frag(l8 + slot * kStage + (BM + wn * (BN / 2)) * kBlk + 2048 * r);
+    else fa[par][r - FN] = frag(l8 + slot * kStage + wm * (BM / 2) * kBlk + 2048 * (r - FN));
+  };
+  static_for<RING - 1>([&](auto S_) { scales(decltype(S_)::value, S_); });
+  static_for<SLOTS>([&](auto S_) {
+    static_for<LA + LB>([&](auto I_) { issue(decltype(S_)::value, decltype(S_)::value, I_); });
   });
-  // step s: the stage's loads are done (the newer stages' may fly) and
-  // every wave is past its reads of stage s - 1, whose slot is refilled
-  auto step = [&](int s, int slot) {
-    wait_vmcnt<(SLOTS - 2) * (LA + LB + 2)>();
+  wait_vmcnt<(SLOTS - 1) * (LA + LB)>();
+  block_sync_lds();
+  static_for<FM + FN>([&](auto R_) { read(0, std::integral_constant<int, 0>{}, R_); });
+  // step s (J: its index mod UNROLL): stage s is in registers, stage s + 1
+  // has landed (newer ones may fly), and stage s + SLOTS goes into the slot
+  // of stage s, which every wave is past reading. Loads and the reads of
+  // stage s + 1 are spread over the step's MFMAs.
+  auto step = [&](auto J_, int s) {
+    constexpr int J = decltype(J_)::value, P = J & 1;
+    __builtin_amdgcn_sched_barrier(0);
+    // (loads of scales may lie anywhere among these, so they are not counted)
+    wait_vmcnt<(SLOTS - 2) * (LA + LB)>();
     block_sync_lds();
-    const u32x2 ca = xa[0], cb = xb[0];
-#pragma unroll
-    for (int i = 0; i + 1 < SLOTS - 1; ++i) {
-      xa[i] = xa[i + 1];
-      xb[i] = xb[i + 1];
-    }
-    xa[SLOTS - 2] = scale_load(p.sa, asz, soffa, kblock(s + SLOTS - 1) * (int)p.sra, FMc{});
-    xb[SLOTS - 2] = scale_load(p.sb, bsz, soffb, kblock(s + SLOTS - 1) * (int)p.srb, FNc{});
-    issue(slot == 0 ? SLOTS - 1 : slot - 1, s + SLOTS - 1);
-    const lds_u8* la = l8 + slot * kStage + wm * (BM / 2) * kBlk;
-    const lds_u8* lb = l8 + slot * kStage + (BM + wn * (BN / 2)) * kBlk;
-    v8i fb[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = frag(lb + 2048 * j);
-    static_for<FM>([&](auto I_) {
-      constexpr int i = decltype(I_)::value;
-      const v8i fa = frag(la + 2048 * i);
-      static_for<FN>([&](auto J_) {
-        constexpr int j = decltype(J_)::value;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, acc[i][j], FMT_B, FMT_A, j & 3,
-                                                                     (int)cb[j >> 2], i & 3, (int)ca[i >> 2]);
+    scales(s + RING - 1, std::integral_constant<int, (J + RING - 1) % RING>{});
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<FM * FN>([&](auto T_) {
+      constexpr int t = decltype(T_)::value, i = t / FN, j = t % FN;
+      constexpr int kReads = FM + FN, kMfma = FM * FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[P][j], fa[P][i], acc[i][j], FMT_B, FMT_A, j & 3,
+                                                                   (int)xb[J % RING][j >> 2], i & 3,
+                                                                   (int)xa[J % RING][i >> 2]);
+      constexpr int r0 = t * kReads / kMfma, r1 = (t + 1) * kReads / kMfma;
+      static_for<r1 - r0>([&](auto R_) {
+        read((J + 1) % SLOTS, std::integral_constant<int, P ^ 1>{}, std::integral_constant<int, r0 + decltype(R_)::value>{});
       });
+      constexpr int l0 = t * (LA + LB) / kMfma, l1 = (t + 1) * (LA + LB) / kMfma;
+      static_for<l1 - l0>([&](auto L_) {
+        issue(J % SLOTS, s + SLOTS, std::integral_constant<int, l0 + decltype(L_)::value>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
     });
   };
-  int slot = 0;
-  for (int s = 0; s < nk; ++s) {
-    step(s, slot);
-    slot = slot + 1 == SLOTS ? 0 : slot + 1;
-  }
+  int s = 0;
+  for (; s + UNROLL <= nk; s += UNROLL)
+    static_for<UNROLL>([&](auto J_) { step(J_, s + decltype(J_)::value); });
+  const int rest = nk - s;
+  static_for<UNROLL - 1>([&](auto J_) {
+    if (decltype(J_)::value < rest) step(J_, s + decltype(J_)::value);
+  });
   wait_vmcnt<0>();
   block_sync_lds();
 
@@ -292,7 +318,7 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
 }
 
 template <int FMT_A, int FMT_B, int BM, int BN, int SLOTS>
-__global__ __launch_bounds__(256) void block_gemm_kernel(Problem p) {
+__global__ __launch_bounds__(256, (BM + BN) * SLOTS > 640 ? 1 : 2) void block_gemm_kernel(Problem p) {
   gemm_tile<FMT_A, FMT_B, BM, BN, SLOTS>(p);
 }
 
@@ -574,39 +600,50 @@ __global__ __launch_bounds__(256) void block_gemm_join_kernel(Problem p) {
                     p.ldc, p.M, p.N, tm * BM + (w >> 1) * (BM / 2) + 16 * i, tn * BN + (w & 1) * (BN / 2));
 }
 
-// The tile and the split of a product: the least estimated time. A tile's
-// k-block takes its workgroup a time that depends on how many share a CU
-// (`rounds` of 256, or of 512 where two fit); a split adds the join's launch
-// and its FP32 partials' way to memory and back. Times measured at nk = 8 ..
-// 160 k-blocks; the estimate is within 15 % of them. What each tile is for
-// (us, measured; s: split in that many):
-//                          256x256      128x128     128x64      64x64
-//   2048 x 20480 x 4096    139          168         -           -
-//   2048 x 4096 x 20480    160, s2 128  159         -           -
-//   333 x 15360 x 5120     51, s2 49    41          48          59
-//   2000 x 2000 x 4000     40, s2 35    27          24          32
-//   997 x 2002 x 1200      23           11, s2 16   7.9         8.4
-//   64 x 12288 x 4096      38, s3 29    26, s4 20   18          15
+// The tile and the split of a product: the least estimated time. Workgroups
+// go out in rounds of 256, one a CU, and a k-block takes a round a time of
+// its own, less in a round that half fills the chip (the CUs' shares of L2
+// and of the power limit are larger). A split adds the join's launch and
+// its FP32 partials' way to memory and back. The times are fits to products
+// of 8 .. 288 k-blocks, most within 10 % (256 x 128 by its pace among other
+// products, 0.85: alone it runs faster, 0.75, than its LDS reads let it under
+// the power limit). What each tile is for (us, alone; s: the reduction in
+// that many):
+//                          256x256       256x128      128x128   128x64    64x64
+//   2048 x 36864 x 12288   690           790          1077
+//   2048 x 12288 x 36864   676, s2 639   774          986
+//   2048 x 10240 x 4096    86            79           84        115       134
+//   2048 x 4096 x 20480    157, s2 129   124          150       201       271
+//   333 x 15360 x 5120     47            32           43        45        54
+//   1024 x 4096 x 8192     66, s2 47     42, s2 39    32
+//   997 x 2002 x 1200      22            13           8.9       7.2       8.2
+//   64 x 12288 x 4096      38, s3 29     23           15        13        12
 struct Plan {
   int bm, bn, splits;
 };
 inline Plan plan(int64_t M, int64_t N, int64_t nk, bool may_split) {
   struct Tile {
-    int bm, bn, per_cu;
-    float one, full;  // us a k-block: at most one workgroup a CU; every CU full
+    int bm, bn;
+    float fixed;              // us: launch, first loads, stores
+    float half, whole, more;  // us a k-block of a round: of at most 128; of 256; of 256 among several
   };
-  constexpr Tile kTiles[] = {{256, 256, 1, 1.45f, 1.45f}, {128, 128, 2, 0.73f, 1.05f}, {128, 64, 2, 0.43f, 0.65f},
-                             {64, 64, 2, 0.34f, 0.50f}};
+  constexpr Tile kTiles[] = {{256, 256, 5.0f, 1.04f, 1.45f, 1.45f},
+                             {256, 128, 5.0f, 0.66f, 0.85f, 0.87f},
+                             {128, 128, 3.8f, 0.43f, 0.45f, 0.55f},
+                             {128, 64, 3.5f, 0.29f, 0.31f, 0.36f},
+                             {64, 64, 3.2f, 0.23f, 0.27f, 0.24f}};
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   Plan best{256, 256, 1};
   float least = 1e30f;
   for (const Tile& t : kTiles) {
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn);
     for (int s : kSplits) {
-      if (s > 1 && (!may_split || s > nk / 3 || tiles * s > 512)) break;
-      const int64_t n = tiles * s, round = 256 * t.per_cu;
-      const float per = n <= 256 ? t.one : t.full * (float)((n + round - 1) / round);
-      const float us = 3.0f + (float)((nk + s - 1) / s) * per + (s > 1 ? 4.0f + 1e-6f * (float)M * (float)N * s : 0.0f);
+      if (s > 1 && (!may_split || s > nk / 3 || tiles * s > 1024)) break;
+      const int64_t n = tiles * s, full = n / 256, rest = n % 256;
+      const float round = n <= 256 ? (n <= 128 ? t.half : t.whole)
+                                   : (float)full * t.more + (rest == 0 ? 0.0f : rest <= 128 ? t.half : t.more);
+      const float us = t.fixed + (float)((nk + s - 1) / s) * round +
+                       (s > 1 ? 3.0f + 0.7e-6f * (float)M * (float)N * (float)s : 0.0f);
       if (us < least) {
         least = us;
         best = {t.bm, t.bn, s};
@@ -621,14 +658,17 @@ hipError_t run(const Problem& p, int bm, int bn, hipStream_t st) {
   const int ntiles = p.tiles_m * p.tiles_n;
   const dim3 grid(ntiles * p.splits);
   const bool join = p.splits > 1;
-  if (bm == kBig) {
+  if (bn == 256) {
     block_gemm_big_kernel<FA, FB><<<grid, 256, 0, st>>>(p);
     if (join) block_gemm_join_kernel<256, 256><<<dim3(ntiles, 8), 256, 0, st>>>(p);
+  } else if (bm == 256) {
+    block_gemm_kernel<FA, FB, 256, 128, 3><<<grid, 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<256, 128><<<dim3(ntiles, 8), 256, 0, st>>>(p);
   } else if (bn == 128) {
-    block_gemm_kernel<FA, FB, 128, 128, 2><<<grid, 256, 0, st>>>(p);
+    block_gemm_kernel<FA, FB, 128, 128, 4><<<grid, 256, 0, st>>>(p);
     if (join) block_gemm_join_kernel<128, 128><<<dim3(ntiles, 4), 256, 0, st>>>(p);
   } else if (bm == 128) {
-    block_gemm_kernel<FA, FB, 128, 64, 3><<<grid, 256, 0, st>>>(p);
+    block_gemm_kernel<FA, FB, 128, 64, 4><<<grid, 256, 0, st>>>(p);
     if (join) block_gemm_join_kernel<128, 64><<<dim3(ntiles, 4), 256, 0, st>>>(p);
   } else {
     block_gemm_kernel<FA, FB, 64, 64, 4><<<grid, 256, 0, st>>>(p);
