@@ -211,8 +211,8 @@ def _space(n: int, device) -> torch.Tensor:
     return torch.empty(n, dtype=_U8, device=device)
 
 
-def _flags(needs) -> int:
-    return sum(f for f, n in zip((FP8_BLOCK_NEED_DX, FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2), needs) if n)
+def _flags(dx: bool, dw: bool, dw2: bool = False) -> int:
+    return (FP8_BLOCK_NEED_DX if dx else 0) | (FP8_BLOCK_NEED_DW if dw else 0) | (FP8_BLOCK_NEED_DW2 if dw2 else 0)
 
 
 def _wants_grad(*tensors) -> bool:
@@ -230,7 +230,7 @@ def _linear_fwd(X, W, flags):
     dev = X.device
     kept = _space(nk, dev) if flags else None
     scratch = _space(nf, dev)
-    Y = torch.empty((*X.shape[:-1], N), dtype=_BF16, device=dev)
+    Y = torch.empty((M, N) if X2 is X else (*X.shape[:-1], N), dtype=_BF16, device=dev)
     check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, flags, kept.data_ptr() if flags else None, nk,
                                       scratch.data_ptr(), nf, Y.data_ptr(), _on(X)), "fp8_block_linear_fwd")
     return Y, kept, (M, K, N)
@@ -239,7 +239,7 @@ def _linear_fwd(X, W, flags):
 class _BlockLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W):
-        flags = _flags(ctx.needs_input_grad)
+        flags = _flags(*ctx.needs_input_grad)
         Y, kept, ctx.size = _linear_fwd(X, W, flags)
         ctx.save_for_backward(kept)
         ctx.flags, ctx.lead = flags, X.shape[:-1]
@@ -394,7 +394,7 @@ def _mlp_fwd(X, Wgu, Wd, flags):
 class _BlockMlpFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, Wgu, Wd):
-        flags = _flags(ctx.needs_input_grad)
+        flags = _flags(*ctx.needs_input_grad)
         Y, kept, ctx.size = _mlp_fwd(X, Wgu, Wd, flags)
         ctx.save_for_backward(kept)
         ctx.flags, ctx.shape = flags, X.shape
