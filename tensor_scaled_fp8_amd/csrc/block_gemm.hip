@@ -77,8 +77,9 @@ struct Problem {
   int64_t sra, srb;      // scale bytes of a k-block
   int M, N, nk;          // nk: k-blocks
   int tiles_m, tiles_n;
-  int splits;            // workgroups of a tile; split s takes k-blocks [s nk / splits, (s + 1) nk / splits)
-  float* part;           // splits > 1: FP32 partials
+  int whole;             // the first tiles: one workgroup each
+  int splits;            // workgroups of each other tile; split s takes k-blocks [s nk / splits, (s + 1) nk / splits)
+  float* part;           // their FP32 partials
 };
 
 // tile order: workgroups are dealt round-robin to the 8 XCDs; each XCD gets
@@ -157,12 +158,17 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
   __shared__ uint4 lds[SLOTS * kStage / 16];
   lds_u8* const l8 = (lds_u8*)lds;
 
-  const int ntiles = p.tiles_m * p.tiles_n;
-  const int split = blockIdx.x / ntiles;
+  int pid = blockIdx.x, split = 0, splits = 1;
+  if (pid >= p.whole) {
+    const int shared = p.tiles_m * p.tiles_n - p.whole;
+    split = (pid - p.whole) / shared;
+    splits = p.splits;
+    pid -= split * shared;
+  }
   int tm, tn;
-  tile_origin(blockIdx.x - split * ntiles, p.tiles_m, p.tiles_n, tm, tn);
+  tile_origin(pid, p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  const int k0 = (int)((int64_t)split * p.nk / p.splits), k1 = (int)((int64_t)(split + 1) * p.nk / p.splits);
+  const int k0 = (int)((int64_t)split * p.nk / splits), k1 = (int)((int64_t)(split + 1) * p.nk / splits);
   const int nk = k1 - k0;
 
   const int t = threadIdx.x, lane = t & 63;
@@ -301,9 +307,9 @@ __device__ __forceinline__ void gemm_tile(const Problem& p) {
   wait_vmcnt<0>();
   block_sync_lds();
 
-  if (p.splits > 1) {
+  if (splits > 1) {
     // partials in register order: float4 (i FN + j) of thread t
-    float* d = p.part + ((int64_t)split * ntiles + (tm * p.tiles_n + tn)) * (BM * BN) + 4 * t;
+    float* d = p.part + (int64_t)(blockIdx.x - p.whole) * (BM * BN) + 4 * t;
     static_for<FM>([&](auto I_) {
       static_for<FN>([&](auto J_) {
         constexpr int i = decltype(I_)::value, j = decltype(J_)::value;
@@ -366,12 +372,17 @@ __device__ __forceinline__ void mfma_into(f32x4& c, const v8i& b, const v8i& a, 
 
 template <int FMT_A, int FMT_B>
 __device__ __forceinline__ void gemm_tile_big(const Problem& p) {
-  const int ntiles = p.tiles_m * p.tiles_n;
-  const int split = blockIdx.x / ntiles;
+  int pid = blockIdx.x, split = 0, splits = 1;
+  if (pid >= p.whole) {
+    const int shared = p.tiles_m * p.tiles_n - p.whole;
+    split = (pid - p.whole) / shared;
+    splits = p.splits;
+    pid -= split * shared;
+  }
   int tm, tn;
-  tile_origin(blockIdx.x - split * ntiles, p.tiles_m, p.tiles_n, tm, tn);
+  tile_origin(pid, p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * kBig, n0 = tn * kBig;
-  const int k0 = (int)((int64_t)split * p.nk / p.splits), k1 = (int)((int64_t)(split + 1) * p.nk / p.splits);
+  const int k0 = (int)((int64_t)split * p.nk / splits), k1 = (int)((int64_t)(split + 1) * p.nk / splits);
   const int nk = k1 - k0;
 
   const int t = threadIdx.x, lane = t & 63;
@@ -560,8 +571,8 @@ __device__ __forceinline__ void gemm_tile_big(const Problem& p) {
   // k-loop, where registers are full)
   int te = t;
   asm volatile("" : "+v"(te));
-  if (p.splits > 1) {
-    float* d = p.part + ((int64_t)split * ntiles + (tm * p.tiles_n + tn)) * (kBig * kBig) + 4 * te;
+  if (splits > 1) {
+    float* d = p.part + (int64_t)(blockIdx.x - p.whole) * (kBig * kBig) + 4 * te;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -583,10 +594,11 @@ template <int BM, int BN>
 __global__ __launch_bounds__(256) void block_gemm_join_kernel(Problem p) {
   constexpr int FN = BN / 32;
   __shared__ uint4 lds[4 * 32 * FN];
-  const int tile = blockIdx.x, i = blockIdx.y;
-  const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
+  const int tile = blockIdx.x, i = blockIdx.y;  // the tile of those that are shared
+  int tm, tn;
+  tile_origin(p.whole + tile, p.tiles_m, p.tiles_n, tm, tn);
   const int t = threadIdx.x, w = t >> 6;
-  const int64_t stride = (int64_t)p.tiles_m * p.tiles_n * (BM * BN);
+  const int64_t stride = (int64_t)(p.tiles_m * p.tiles_n - p.whole) * (BM * BN);
   const float* s = p.part + (int64_t)tile * (BM * BN) + 1024 * (i * FN) + 4 * t;
   f32x4 acc[FN];
 #pragma unroll
@@ -603,12 +615,15 @@ __global__ __launch_bounds__(256) void block_gemm_join_kernel(Problem p) {
 // The tile and the split of a product: the least estimated time. Workgroups
 // go out in rounds of 256, one a CU, and a k-block takes a round a time of
 // its own, less in a round that half fills the chip (the CUs' shares of L2
-// and of the power limit are larger). A split adds the join's launch and
-// its FP32 partials' way to memory and back. The times are fits to products
-// of 8 .. 288 k-blocks, most within 10 % (256 x 128 by its pace among other
-// products, 0.85: alone it runs faster, 0.75, than its LDS reads let it under
-// the power limit). What each tile is for (us, alone; s: the reduction in
-// that many):
+// and of the power limit are larger). Tiles of full rounds have a workgroup
+// each; those of a last round that is not full may have several, which adds
+// the join's launch and their FP32 partials' way to memory and back. The
+// times are fits to products of 8 .. 288 k-blocks, most within 10 % (256 x
+// 128 by its pace among other products, 0.85: alone it runs faster, 0.75,
+// than its LDS reads let it under the power limit). The shared last round
+// took the GPT-175B qkv dX from 633 to 601 us and the forward from 706 to
+// 692, a 2048 x 10240 x 4096 product from 96 to 95. What each tile is for
+// (us, alone; s: the reduction in that many):
 //                          256x256       256x128      128x128   128x64    64x64
 //   2048 x 36864 x 12288   690           790          1077
 //   2048 x 12288 x 36864   676, s2 639   774          986
@@ -637,13 +652,16 @@ inline Plan plan(int64_t M, int64_t N, int64_t nk, bool may_split) {
   float least = 1e30f;
   for (const Tile& t : kTiles) {
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn);
+    const int64_t full = tiles / 256, rest = tiles % 256;
+    const float round = tiles <= 256 ? t.whole : t.more;
     for (int s : kSplits) {
-      if (s > 1 && (!may_split || s > nk / 3 || tiles * s > 1024)) break;
-      const int64_t n = tiles * s, full = n / 256, rest = n % 256;
-      const float round = n <= 256 ? (n <= 128 ? t.half : t.whole)
-                                   : (float)full * t.more + (rest == 0 ? 0.0f : rest <= 128 ? t.half : t.more);
-      const float us = t.fixed + (float)((nk + s - 1) / s) * round +
-                       (s > 1 ? 3.0f + 0.7e-6f * (float)M * (float)N * (float)s : 0.0f);
+      const int64_t n = rest * s;  // workgroups after the full rounds
+      if (s > 1 && (!may_split || rest == 0 || s > nk / 3 || n > 1024)) break;
+      const float part = (float)(n % 256);
+      const float last = (float)(n / 256) * t.more +
+                         (part == 0 ? 0.0f : part <= 128 ? t.half : t.half + (round - t.half) * (part - 128.0f) / 128.0f);
+      const float us = t.fixed + (float)nk * (float)full * round + (float)((nk + s - 1) / s) * last +
+                       (s > 1 ? 3.0f + 0.7e-6f * (float)(n * t.bm * t.bn) : 0.0f);
       if (us < least) {
         least = us;
         best = {t.bm, t.bn, s};
@@ -655,24 +673,24 @@ inline Plan plan(int64_t M, int64_t N, int64_t nk, bool may_split) {
 
 template <int FA, int FB>
 hipError_t run(const Problem& p, int bm, int bn, hipStream_t st) {
-  const int ntiles = p.tiles_m * p.tiles_n;
-  const dim3 grid(ntiles * p.splits);
-  const bool join = p.splits > 1;
+  const int shared = p.tiles_m * p.tiles_n - p.whole;
+  const dim3 grid(p.whole + shared * p.splits);
+  const bool join = shared > 0;
   if (bn == 256) {
     block_gemm_big_kernel<FA, FB><<<grid, 256, 0, st>>>(p);
-    if (join) block_gemm_join_kernel<256, 256><<<dim3(ntiles, 8), 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<256, 256><<<dim3(shared, 8), 256, 0, st>>>(p);
   } else if (bm == 256) {
     block_gemm_kernel<FA, FB, 256, 128, 3><<<grid, 256, 0, st>>>(p);
-    if (join) block_gemm_join_kernel<256, 128><<<dim3(ntiles, 8), 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<256, 128><<<dim3(shared, 8), 256, 0, st>>>(p);
   } else if (bn == 128) {
     block_gemm_kernel<FA, FB, 128, 128, 4><<<grid, 256, 0, st>>>(p);
-    if (join) block_gemm_join_kernel<128, 128><<<dim3(ntiles, 4), 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<128, 128><<<dim3(shared, 4), 256, 0, st>>>(p);
   } else if (bm == 128) {
     block_gemm_kernel<FA, FB, 128, 64, 4><<<grid, 256, 0, st>>>(p);
-    if (join) block_gemm_join_kernel<128, 64><<<dim3(ntiles, 4), 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<128, 64><<<dim3(shared, 4), 256, 0, st>>>(p);
   } else {
     block_gemm_kernel<FA, FB, 64, 64, 4><<<grid, 256, 0, st>>>(p);
-    if (join) block_gemm_join_kernel<64, 64><<<dim3(ntiles, 2), 256, 0, st>>>(p);
+    if (join) block_gemm_join_kernel<64, 64><<<dim3(shared, 2), 256, 0, st>>>(p);
   }
   return hipGetLastError();
 }
@@ -683,7 +701,8 @@ size_t block_gemm_ws_bytes(int64_t M, int64_t N, int64_t R) {
   if (M <= 0 || N <= 0) return 0;
   const Plan q = plan(M, N, round_blk(R) / kBlk, true);
   if (q.splits <= 1) return 0;
-  return (size_t)q.splits * ((M + q.bm - 1) / q.bm * q.bm) * ((N + q.bn - 1) / q.bn * q.bn) * 4;
+  const int64_t tiles = ((M + q.bm - 1) / q.bm) * ((N + q.bn - 1) / q.bn);
+  return (size_t)(tiles % 256) * q.splits * q.bm * q.bn * 4;
 }
 
 hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipStream_t st) {
@@ -707,6 +726,8 @@ hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipS
   p.tiles_m = (int)((M + q.bm - 1) / q.bm);
   p.tiles_n = (int)((N + q.bn - 1) / q.bn);
   p.splits = q.splits;
+  p.whole = p.tiles_m * p.tiles_n;
+  if (q.splits > 1) p.whole -= p.whole % 256;
   p.part = (float*)ws;
   if (g.fa == FP8_E5M2) return g.fb == FP8_E5M2 ? run<1, 1>(p, q.bm, q.bn, st) : run<1, 0>(p, q.bm, q.bn, st);
   return g.fb == FP8_E5M2 ? run<0, 1>(p, q.bm, q.bn, st) : run<0, 0>(p, q.bm, q.bn, st);

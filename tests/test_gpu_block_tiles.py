@@ -25,7 +25,7 @@ def _stored(g, rows, cols, fmt):
 SIZES = [(4000, 4100, 390), (4096, 4096, 500), (3900, 4000, 640), (1000, 8000, 640), (2000, 2100, 1200),
          (4000, 4100, 1300), (1800, 4000, 3000), (1000, 8000, 130), (2048, 2048, 300), (1900, 2001, 900),
          (1500, 6000, 700), (3000, 3001, 1400), (1024, 2048, 700), (997, 2002, 1200), (1000, 2000, 1025),
-         (333, 2222, 1111), (60, 500, 6000), (513, 1030, 4000), (1100, 1100, 10000), (1500, 3000, 6000),
+         (4100, 4100, 3000), (2300, 8000, 2500), (333, 2222, 1111), (60, 500, 6000), (513, 1030, 4000), (1100, 1100, 10000), (1500, 3000, 6000),
          (2048, 4096, 20480)]
 
 
