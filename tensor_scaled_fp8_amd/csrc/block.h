@@ -42,6 +42,15 @@ struct Bf16Mat {
 
 hipError_t launch_block_quantize(const Bf16Mat& x, int fmt, const BlockMat& row, const BlockMat& t, int64_t t_row0,
                                  hipStream_t st);
+// E4M3 forms of up to kMaxQuant matrices, by one launch where all want both
+// forms (a training step's X and weights: two launches of 2 us each on the
+// host less in an MLP)
+constexpr int kMaxQuant = 3;
+struct BlockQuant {
+  Bf16Mat x;
+  BlockMat row, t;
+};
+hipError_t launch_block_quantize_many(const BlockQuant* q, int n, hipStream_t st);
 hipError_t launch_block_dequantize(const BlockMat& q, int fmt, uint16_t* out, int64_t ld, hipStream_t st);
 
 // C [M, N] bf16 (row pitch ldc) = sum over k of A(m, k) B(n, k): A [M, R]

@@ -260,8 +260,8 @@ fp8_status fp8_block_linear_fwd(const void* X, int64_t ldx, const void* W, int64
   const LinearKept k(kept, M, K, N, flags);
   const LinearFwd f(scratch, M, K, N, true);
   if (!space_ok(kept, kept_bytes, k.bytes) || !space_ok(scratch, scratch_bytes, f.bytes)) return FP8_ERR_INVALID;
-  TRY(launch_block_quantize({(const uint16_t*)X, ldx, M, K}, FP8_E4M3, f.x, k.xt, 0, stream));
-  TRY(launch_block_quantize({(const uint16_t*)W, ldw, K, N}, FP8_E4M3, k.w, f.wt, 0, stream));
+  const BlockQuant q[] = {{{(const uint16_t*)X, ldx, M, K}, f.x, k.xt}, {{(const uint16_t*)W, ldw, K, N}, k.w, f.wt}};
+  TRY(launch_block_quantize_many(q, 2, stream));
   return hip_status(launch_block_gemm({f.x, f.wt, FP8_E4M3, FP8_E4M3, (uint16_t*)Y, N}, f.part, f.part_bytes, stream));
 }
 
@@ -370,12 +370,14 @@ fp8_status fp8_block_mlp_fwd(const void* X, int64_t ldx, const void* Wgu, int64_
   const MlpKept k(kept, M, K, F, flags);
   const MlpFwd f(scratch, M, K, F);
   if (!space_ok(kept, kept_bytes, k.bytes) || !space_ok(scratch, scratch_bytes, f.bytes)) return FP8_ERR_INVALID;
-  TRY(launch_block_quantize({(const uint16_t*)X, ldx, M, K}, FP8_E4M3, f.x, k.xt, 0, stream));
   const uint16_t* w = (const uint16_t*)Wgu;
+  const BlockQuant q[] = {{{(const uint16_t*)X, ldx, M, K}, f.x, k.xt},
+                          {{(const uint16_t*)Wd, ldwd, F, K}, k.wd, f.wdt},
+                          {{w, ldwgu, K, 2 * F}, k.wgu, f.wgut}};
   if (F % kBlk == 0 || !k.wgu.codes) {
-    BlockMat row = k.wgu;
-    TRY(launch_block_quantize({w, ldwgu, K, 2 * F}, FP8_E4M3, row, f.wgut, 0, stream));
+    TRY(launch_block_quantize_many(q, 3, stream));
   } else {
+    TRY(launch_block_quantize_many(q, 2, stream));
     // a half's blocks start at its own first column
     for (int i = 0; i < 2; ++i) {
       BlockMat t = f.wgut;
@@ -383,7 +385,6 @@ fp8_status fp8_block_mlp_fwd(const void* X, int64_t ldx, const void* Wgu, int64_
       TRY(launch_block_quantize({w + i * F, ldwgu, K, F}, FP8_E4M3, half(k.wgu, F, i), t, i * F, stream));
     }
   }
-  TRY(launch_block_quantize({(const uint16_t*)Wd, ldwd, F, K}, FP8_E4M3, k.wd, f.wdt, 0, stream));
   TRY(launch_block_gemm({f.x, f.wgut, FP8_E4M3, FP8_E4M3, f.gu, 2 * F}, f.part, f.part_bytes, stream));
   TRY(launch_swiglu_fwd({f.gu, 2 * F, M, F}, {f.gu + F, 2 * F, M, F}, nullptr, 0, f.h, k.g, k.u, stream));
   return hip_status(launch_block_gemm({f.h, f.wdt, FP8_E4M3, FP8_E4M3, (uint16_t*)Y, K}, f.part, f.part_bytes, stream));

@@ -16,13 +16,13 @@ namespace {
 // column's in 16 lane groups of all four waves: its maximum is reduced
 // within a wave, then over LDS by one thread a column.
 template <int FMT, bool ROW>
-__global__ __launch_bounds__(256) void block_quant_tile_kernel(Bf16Mat x, BlockMat row, BlockMat tr, int64_t t_row0,
-                                                               int tiles_c) {
+__device__ __forceinline__ void quant_tile(const Bf16Mat& x, const BlockMat& row, const BlockMat& tr, int64_t t_row0,
+                                           int tiles_c, int at) {
   __shared__ uint4 tile[kBlk * kBlk / 16];
   __shared__ uint32_t cmax[4][kBlk / 2];  // of each wave, two columns' bf16 magnitudes a dword
   __shared__ float cscale[kBlk];
   __shared__ uint8_t rbyte[kBlk];         // in the scales' order
-  const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * kBlk, c0 = (int64_t)(blockIdx.x % tiles_c) * kBlk;
+  const int64_t r0 = (int64_t)(at / tiles_c) * kBlk, c0 = (int64_t)(at % tiles_c) * kBlk;
   const int t = threadIdx.x, rg = t >> 4, cc = t & 15;
   const int64_t rr = r0 + 8 * rg, cx = c0 + 8 * cc;
   bq_u32x4 w[8];
@@ -86,6 +86,26 @@ __global__ __launch_bounds__(256) void block_quant_tile_kernel(Bf16Mat x, BlockM
   }
   __syncthreads();
   put_tile<256>(tile, tr, t_row0 + c0, tr.rows - c0, r0);
+}
+
+template <int FMT, bool ROW>
+__global__ __launch_bounds__(256) void block_quant_tile_kernel(Bf16Mat x, BlockMat row, BlockMat tr, int64_t t_row0,
+                                                               int tiles_c) {
+  quant_tile<FMT, ROW>(x, row, tr, t_row0, tiles_c, blockIdx.x);
+}
+
+// both forms of several matrices: first[i] is the first workgroup of the i-th
+struct QuantSets {
+  BlockQuant q[kMaxQuant];
+  int tiles_c[kMaxQuant], first[kMaxQuant];
+};
+template <int FMT>
+__global__ __launch_bounds__(256) void block_quant_many_kernel(QuantSets s) {
+  int i = 0;
+#pragma unroll
+  for (int k = 1; k < kMaxQuant; ++k) i += (int)blockIdx.x >= s.first[k];
+  const BlockQuant& q = s.q[i];
+  quant_tile<FMT, true>(q.x, q.row, q.t, 0, s.tiles_c[i], blockIdx.x - s.first[i]);
 }
 
 // row form only: 16 RPT rows x 128 columns per workgroup
@@ -164,6 +184,31 @@ hipError_t launch_block_quantize(const Bf16Mat& x, int fmt, const BlockMat& row,
                                  hipStream_t st) {
   if (x.rows == 0 || x.cols == 0 || (!row.codes && !t.codes)) return hipSuccess;
   return fmt == FP8_E5M2 ? quantize<FP8_E5M2>(x, row, t, t_row0, st) : quantize<FP8_E4M3>(x, row, t, t_row0, st);
+}
+
+hipError_t launch_block_quantize_many(const BlockQuant* q, int n, hipStream_t st) {
+  QuantSets s = {};
+  int64_t tiles = 0;
+  bool one = n <= kMaxQuant;
+  for (int i = 0; i < n && one; ++i) {
+    const Bf16Mat& x = q[i].x;
+    one = x.rows > 0 && x.cols > 0 && q[i].row.codes && q[i].t.codes;
+    s.q[i] = q[i];
+    s.tiles_c[i] = (int)((x.cols + kBlk - 1) / kBlk);
+    s.first[i] = (int)tiles;
+    tiles += (x.rows + kBlk - 1) / kBlk * s.tiles_c[i];
+    one = one && tiles < ((int64_t)1 << 23);  // 2^31 threads
+  }
+  if (!one) {
+    for (int i = 0; i < n; ++i) {
+      const hipError_t e = launch_block_quantize(q[i].x, FP8_E4M3, q[i].row, q[i].t, 0, st);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  for (int i = n; i < kMaxQuant; ++i) s.first[i] = 0x7FFFFFFF;
+  block_quant_many_kernel<FP8_E4M3><<<dim3((unsigned)tiles), 256, 0, st>>>(s);
+  return hipGetLastError();
 }
 
 hipError_t launch_block_dequantize(const BlockMat& q, int fmt, uint16_t* out, int64_t ld, hipStream_t st) {
