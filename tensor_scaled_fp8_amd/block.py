@@ -1,7 +1,7 @@
 """Block-scaled FP8: a power-of-two scale for each block of 128 elements.
 
 Python binding of the block entry points of include/fp8lin.h, and their
-autograd forms:
+autograd forms (compiled nodes, csrc/block_autograd.cpp):
 
   fp8_block_quantize / fp8_block_dequantize   8-bit store and restore
   fp8_block_gemm                              product of two stored matrices
@@ -22,7 +22,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import (FP8_BLOCK_NEED_DW, FP8_BLOCK_NEED_DW2, FP8_BLOCK_NEED_DX, check, load)
+from ._lib import check, load
 from .binding import _fmt, _stream
 
 BLOCK = 128
@@ -199,68 +199,32 @@ def _cached_bytes(M: int, K: int, N: int) -> int:
     return 0 if load().fp8_block_linear_few(M, K, N) else load().fp8_block_linear_cached_bytes(M, K, N)
 
 
-@functools.lru_cache(maxsize=4096)
-def _bytes(entry: str, a: int, b: int, c: int, flags: int) -> Tuple[int, int, int]:
-    """Sizes of (kept, forward scratch, backward scratch) of a linear or an MLP."""
-    k, f, w = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
-    check(getattr(load(), entry)(a, b, c, flags, ctypes.byref(k), ctypes.byref(f), ctypes.byref(w)), entry)
-    return k.value, f.value, w.value
-
-
 def _space(n: int, device) -> torch.Tensor:
     return torch.empty(n, dtype=_U8, device=device)
-
-
-def _flags(dx: bool, dw: bool, dw2: bool = False) -> int:
-    return (FP8_BLOCK_NEED_DX if dx else 0) | (FP8_BLOCK_NEED_DW if dw else 0) | (FP8_BLOCK_NEED_DW2 if dw2 else 0)
 
 
 def _wants_grad(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
-def _as_grad(dy: torch.Tensor, name: str):
-    return _as_rows(dy if dy.dtype is _BF16 else dy.to(_BF16), name)
+@functools.lru_cache(maxsize=None)
+def _autograd():
+    """The compiled autograd nodes (csrc/block_autograd.cpp)."""
+    load()
+    try:
+        from . import _block_autograd
+    except ImportError as e:
+        raise ImportError("the block-scaled operators' autograd nodes are not built; build them with "
+                          f"`python -m tensor_scaled_fp8_amd.build` ({e})") from e
+    return _block_autograd
 
 
-def _linear_fwd(X, W, flags):
-    X2, px, ldx, M, K = _as_rows(X, "X")
-    W2, pw, ldw, _, N = _as_rows(W, "W")
-    nk, nf, _ = _bytes("fp8_block_linear_bytes", M, K, N, flags)
-    dev = X.device
-    kept = _space(nk, dev) if flags else None
-    scratch = _space(nf, dev)
-    Y = torch.empty((M, N) if X2 is X else (*X.shape[:-1], N), dtype=_BF16, device=dev)
-    check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, flags, kept.data_ptr() if flags else None, nk,
-                                      scratch.data_ptr(), nf, Y.data_ptr(), _on(X)), "fp8_block_linear_fwd")
-    return Y, kept, (M, K, N)
-
-
-class _BlockLinearFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, X, W):
-        flags = _flags(*ctx.needs_input_grad)
-        Y, kept, ctx.size = _linear_fwd(X, W, flags)
-        ctx.save_for_backward(kept)
-        ctx.flags, ctx.lead = flags, X.shape[:-1]
-        return Y
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dY):
-        kept, = ctx.saved_tensors
-        M, K, N = ctx.size
-        flags = ctx.flags
-        dY, p, ld, _, _ = _as_grad(dY, "dY")
-        dev = dY.device
-        nk, _, nb = _bytes("fp8_block_linear_bytes", M, K, N, flags)
-        scratch = _space(nb, dev)
-        dX = torch.empty((*ctx.lead, K), dtype=_BF16, device=dev) if flags & FP8_BLOCK_NEED_DX else None
-        dW = torch.empty((K, N), dtype=_BF16, device=dev) if flags & FP8_BLOCK_NEED_DW else None
-        check(load().fp8_block_linear_bwd(p, ld, M, K, N, flags, kept.data_ptr(), nk, scratch.data_ptr(), nb,
-                                          None if dX is None else dX.data_ptr(), None if dW is None else dW.data_ptr(),
-                                          _on(dY)), "fp8_block_linear_bwd")
-        return dX, dW
+@functools.lru_cache(maxsize=4096)
+def _forward_bytes(entry: str, a: int, b: int, c: int) -> int:
+    """Scratch of a linear's or an MLP's forward that keeps nothing."""
+    k, f, w = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    check(getattr(load(), entry)(a, b, c, 0, ctypes.byref(k), ctypes.byref(f), ctypes.byref(w)), entry)
+    return f.value
 
 
 def block_linear(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
@@ -270,7 +234,18 @@ def block_linear(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     if X.dim() < 1 or W.dim() != 2 or X.shape[-1] != W.shape[0]:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
     _same_device(X, W, "W")
-    return _BlockLinearFn.apply(X, W) if _wants_grad(X, W) else _linear_fwd(X, W, 0)[0]
+    if _wants_grad(X, W):
+        _check_bf16(X, "X")
+        _check_bf16(W, "W")
+        return _autograd().linear(X, W)
+    X2, px, ldx, M, K = _as_rows(X, "X")
+    W2, pw, ldw, _, N = _as_rows(W, "W")
+    n = _forward_bytes("fp8_block_linear_bytes", M, K, N)
+    scratch = _space(n, X.device)
+    Y = torch.empty((*X.shape[:-1], N), dtype=_BF16, device=X.device)
+    check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr(),
+                                      _on(X)), "fp8_block_linear_fwd")
+    return Y
 
 
 class BlockLinear(torch.nn.Module):
@@ -326,47 +301,6 @@ class BlockInferenceLinear(torch.nn.Module):
         return fp8_block_linear_fwd_cached(_as_rows(x, "x")[0], w).reshape(*x.shape[:-1], self.out_features)
 
 
-def _swiglu_fwd(gate, up, keep):
-    g2, pg, ldg, rows, cols = _as_rows(gate, "gate")
-    u2, pu, ldu, _, _ = _as_rows(up, "up")
-    dev = gate.device
-    n = _swiglu_bytes(rows, cols) if keep else 0
-    kept = _space(n, dev) if keep else None
-    h = torch.empty(gate.shape, dtype=_BF16, device=dev)
-    check(load().fp8_swiglu_fwd(pg, ldg, pu, ldu, rows, cols, h.data_ptr(), kept.data_ptr() if n else None, n,
-                                _on(gate)), "fp8_swiglu_fwd")
-    return h, kept, (rows, cols)
-
-
-@functools.lru_cache(maxsize=4096)
-def _swiglu_bytes(rows: int, cols: int) -> int:
-    return load().fp8_swiglu_kept_bytes(rows, cols)
-
-
-class _SwigluFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, gate, up):
-        h, kept, ctx.size = _swiglu_fwd(gate, up, True)
-        ctx.save_for_backward(kept)
-        ctx.shape = gate.shape
-        return h
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dh):
-        kept, = ctx.saved_tensors
-        rows, cols = ctx.size
-        dh, p, ld, _, _ = _as_grad(dh, "dh")
-        dev = dh.device
-        need = ctx.needs_input_grad
-        dg = torch.empty(ctx.shape, dtype=_BF16, device=dev) if need[0] else None
-        du = torch.empty(ctx.shape, dtype=_BF16, device=dev) if need[1] else None
-        check(load().fp8_swiglu_bwd(p, ld, rows, cols, kept.data_ptr(), kept.numel(),
-                                    None if dg is None else dg.data_ptr(), None if du is None else du.data_ptr(),
-                                    _on(dh)), "fp8_swiglu_bwd")
-        return dg, du
-
-
 def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     """h = gate sigmoid(gate) up, [..., F] bf16. For its backward it keeps
     gate and up in 8 bits (block-scaled E4M3), and computes the gradients at
@@ -374,50 +308,15 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     if gate.shape != up.shape or gate.dim() < 1:
         raise ValueError(f"shape mismatch: gate {tuple(gate.shape)}, up {tuple(up.shape)}")
     _same_device(gate, up, "up")
-    return _SwigluFn.apply(gate, up) if _wants_grad(gate, up) else _swiglu_fwd(gate, up, False)[0]
-
-
-def _mlp_fwd(X, Wgu, Wd, flags):
-    X2, px, ldx, M, K = _as_rows(X, "X")
-    G2, pg, ldg, _, _ = _as_rows(Wgu, "Wgu")
-    D2, pd, ldd, F, _ = _as_rows(Wd, "Wd")
-    dev = X.device
-    nk, nf, _ = _bytes("fp8_block_mlp_bytes", M, K, F, flags)
-    kept = _space(nk, dev) if flags else None
-    scratch = _space(nf, dev)
-    Y = torch.empty(X.shape, dtype=_BF16, device=dev)
-    check(load().fp8_block_mlp_fwd(px, ldx, pg, ldg, pd, ldd, M, K, F, flags, kept.data_ptr() if flags else None, nk,
-                                   scratch.data_ptr(), nf, Y.data_ptr(), _on(X)), "fp8_block_mlp_fwd")
-    return Y, kept, (M, K, F)
-
-
-class _BlockMlpFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, X, Wgu, Wd):
-        flags = _flags(*ctx.needs_input_grad)
-        Y, kept, ctx.size = _mlp_fwd(X, Wgu, Wd, flags)
-        ctx.save_for_backward(kept)
-        ctx.flags, ctx.shape = flags, X.shape
-        return Y
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dY):
-        kept, = ctx.saved_tensors
-        M, K, F = ctx.size
-        flags = ctx.flags
-        dY, p, ld, _, _ = _as_grad(dY, "dY")
-        dev = dY.device
-        nk, _, nb = _bytes("fp8_block_mlp_bytes", M, K, F, flags)
-        scratch = _space(nb, dev)
-        new = dict(dtype=_BF16, device=dev)
-        dX = torch.empty(ctx.shape, **new) if flags & FP8_BLOCK_NEED_DX else None
-        dWgu = torch.empty((K, 2 * F), **new) if flags & FP8_BLOCK_NEED_DW else None
-        dWd = torch.empty((F, K), **new) if flags & FP8_BLOCK_NEED_DW2 else None
-        check(load().fp8_block_mlp_bwd(p, ld, M, K, F, flags, kept.data_ptr(), nk, scratch.data_ptr(), nb,
-                                       *[None if t is None else t.data_ptr() for t in (dX, dWgu, dWd)], _on(dY)),
-              "fp8_block_mlp_bwd")
-        return dX, dWgu, dWd
+    if _wants_grad(gate, up):
+        _check_bf16(gate, "gate")
+        _check_bf16(up, "up")
+        return _autograd().swiglu(gate, up)
+    g2, pg, ldg, rows, cols = _as_rows(gate, "gate")
+    u2, pu, ldu, _, _ = _as_rows(up, "up")
+    h = torch.empty(gate.shape, dtype=_BF16, device=gate.device)
+    check(load().fp8_swiglu_fwd(pg, ldg, pu, ldu, rows, cols, h.data_ptr(), None, 0, _on(gate)), "fp8_swiglu_fwd")
+    return h
 
 
 def block_mlp(X: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor) -> torch.Tensor:
@@ -429,7 +328,19 @@ def block_mlp(X: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor) -> torch.Ten
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wgu {tuple(Wgu.shape)}, Wd {tuple(Wd.shape)}")
     _same_device(X, Wgu, "Wgu")
     _same_device(X, Wd, "Wd")
-    return _BlockMlpFn.apply(X, Wgu, Wd) if _wants_grad(X, Wgu, Wd) else _mlp_fwd(X, Wgu, Wd, 0)[0]
+    if _wants_grad(X, Wgu, Wd):
+        for t, name in ((X, "X"), (Wgu, "Wgu"), (Wd, "Wd")):
+            _check_bf16(t, name)
+        return _autograd().mlp(X, Wgu, Wd)
+    X2, px, ldx, M, K = _as_rows(X, "X")
+    G2, pg, ldg, _, _ = _as_rows(Wgu, "Wgu")
+    D2, pd, ldd, F, _ = _as_rows(Wd, "Wd")
+    n = _forward_bytes("fp8_block_mlp_bytes", M, K, F)
+    scratch = _space(n, X.device)
+    Y = torch.empty(X.shape, dtype=_BF16, device=X.device)
+    check(load().fp8_block_mlp_fwd(px, ldx, pg, ldg, pd, ldd, M, K, F, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr(),
+                                   _on(X)), "fp8_block_mlp_fwd")
+    return Y
 
 
 class BlockMLP(torch.nn.Module):

@@ -1,0 +1,166 @@
+// Autograd nodes of the block-scaled operators: argument layout, memory and
+// one C-ABI call each way. A backward runs on autograd's device thread; as
+// Python there it took 40 us a call more than an empty one where that thread
+// ran on another part of the chip than the caller's, since every object it
+// touches then moves between their caches.
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/extension.h>
+
+#include "fp8lin.h"
+
+namespace {
+
+using at::Tensor;
+using torch::autograd::AutogradContext;
+using torch::autograd::tensor_list;
+
+void check(fp8_status s, const char* what) {
+  if (s != FP8_OK) throw std::runtime_error(std::string(what) + ": " + fp8_status_str(s) + " (status " + std::to_string((int)s) + ")");
+}
+hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.get_device()).stream(); }
+
+// t [..., n] bf16 as a matrix with contiguous rows, a view where it can be
+struct Rows {
+  Tensor t;
+  int64_t ld, rows, cols;
+  explicit Rows(const Tensor& x) : t(x) {
+    if (t.dim() != 2) {
+      const auto s = t.sizes();
+      int64_t n = 1;
+      for (size_t i = 0; i + 1 < s.size(); ++i) n *= s[i];
+      t = t.reshape({n, s.back()});
+    }
+    rows = t.size(0);
+    cols = t.size(1);
+    if (t.stride(1) != 1 && cols > 1) t = t.contiguous();
+    ld = t.stride(0);
+  }
+  const void* p() const { return t.data_ptr(); }
+};
+Rows grad_rows(const Tensor& dy) { return Rows(dy.scalar_type() == at::kBFloat16 ? dy : dy.to(at::kBFloat16)); }
+
+Tensor space(size_t n, const Tensor& like) { return at::empty({(int64_t)n}, like.options().dtype(at::kByte)); }
+Tensor make(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kBFloat16)); }
+void* ptr(const Tensor& t) { return t.defined() && t.numel() ? t.data_ptr() : nullptr; }
+
+// A graph of the gradients themselves (create_graph) is refused when it is
+// used: the kernels' results would be taken for constants.
+tensor_list once(const Tensor& dy, tensor_list out) {
+  if (!at::GradMode::is_enabled() || !dy.requires_grad()) return out;
+  for (Tensor& t : out)
+    if (t.defined()) t = t.detach().set_requires_grad(true);
+  auto err = std::make_shared<torch::autograd::DelayedError>(
+      "trying to differentiate twice a function that was marked with @once_differentiable", (int64_t)out.size());
+  return (*err)(std::move(out));
+}
+
+int flag(const Tensor& t, int f) { return t.requires_grad() ? f : 0; }
+
+struct Linear : torch::autograd::Function<Linear> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& X, const Tensor& W) {
+    const int flags = flag(X, FP8_BLOCK_NEED_DX) | flag(W, FP8_BLOCK_NEED_DW);
+    const Rows x(X), w(W);
+    const int64_t M = x.rows, K = x.cols, N = w.cols;
+    size_t nk, nf, nb;
+    check(fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
+    const Tensor kept = space(nk, X), scratch = space(nf, X);
+    auto shape = X.sizes().vec();
+    shape.back() = N;
+    Tensor Y = make(shape, X);
+    check(fp8_block_linear_fwd(x.p(), x.ld, w.p(), w.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nf, Y.data_ptr(),
+                               stream_of(X)),
+          "fp8_block_linear_fwd");
+    ctx->save_for_backward({kept});
+    ctx->saved_data["flags"] = (int64_t)flags;
+    ctx->saved_data["X"] = X.sizes().vec();
+    ctx->saved_data["N"] = N;
+    return Y;
+  }
+  static tensor_list backward(AutogradContext* ctx, const tensor_list& grads) {
+    const Tensor kept = ctx->get_saved_variables()[0];
+    const int flags = (int)ctx->saved_data["flags"].toInt();
+    const auto shape = ctx->saved_data["X"].toIntVector();
+    const Rows dy = grad_rows(grads[0]);
+    const int64_t M = dy.rows, K = shape.back(), N = ctx->saved_data["N"].toInt();
+    size_t nk, nf, nb;
+    check(fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
+    const Tensor scratch = space(nb, dy.t);
+    Tensor dX, dW;
+    if (flags & FP8_BLOCK_NEED_DX) dX = make(shape, dy.t);
+    if (flags & FP8_BLOCK_NEED_DW) dW = make({K, N}, dy.t);
+    check(fp8_block_linear_bwd(dy.p(), dy.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dW),
+                               stream_of(dy.t)),
+          "fp8_block_linear_bwd");
+    return once(grads[0], {dX, dW});
+  }
+};
+
+struct Swiglu : torch::autograd::Function<Swiglu> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& gate, const Tensor& up) {
+    const Rows g(gate), u(up);
+    const size_t n = fp8_swiglu_kept_bytes(g.rows, g.cols);
+    const Tensor kept = space(n, gate);
+    Tensor h = make(gate.sizes(), gate);
+    check(fp8_swiglu_fwd(g.p(), g.ld, u.p(), u.ld, g.rows, g.cols, h.data_ptr(), ptr(kept), n, stream_of(gate)),
+          "fp8_swiglu_fwd");
+    ctx->save_for_backward({kept});
+    ctx->saved_data["need"] = (int64_t)(flag(gate, 1) | flag(up, 2));
+    return h;
+  }
+  static tensor_list backward(AutogradContext* ctx, const tensor_list& grads) {
+    const Tensor kept = ctx->get_saved_variables()[0];
+    const int need = (int)ctx->saved_data["need"].toInt();
+    const Rows d = grad_rows(grads[0]);
+    Tensor dg, du;
+    if (need & 1) dg = make(grads[0].sizes(), d.t);
+    if (need & 2) du = make(grads[0].sizes(), d.t);
+    check(fp8_swiglu_bwd(d.p(), d.ld, d.rows, d.cols, ptr(kept), (size_t)kept.numel(), ptr(dg), ptr(du), stream_of(d.t)),
+          "fp8_swiglu_bwd");
+    return once(grads[0], {dg, du});
+  }
+};
+
+struct Mlp : torch::autograd::Function<Mlp> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& X, const Tensor& Wgu, const Tensor& Wd) {
+    const int flags = flag(X, FP8_BLOCK_NEED_DX) | flag(Wgu, FP8_BLOCK_NEED_DW) | flag(Wd, FP8_BLOCK_NEED_DW2);
+    const Rows x(X), g(Wgu), d(Wd);
+    const int64_t M = x.rows, K = x.cols, F = d.rows;
+    size_t nk, nf, nb;
+    check(fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
+    const Tensor kept = space(nk, X), scratch = space(nf, X);
+    Tensor Y = make(X.sizes(), X);
+    check(fp8_block_mlp_fwd(x.p(), x.ld, g.p(), g.ld, d.p(), d.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nf,
+                            Y.data_ptr(), stream_of(X)),
+          "fp8_block_mlp_fwd");
+    ctx->save_for_backward({kept});
+    ctx->saved_data["flags"] = (int64_t)flags;
+    ctx->saved_data["F"] = F;
+    return Y;
+  }
+  static tensor_list backward(AutogradContext* ctx, const tensor_list& grads) {
+    const Tensor kept = ctx->get_saved_variables()[0];
+    const int flags = (int)ctx->saved_data["flags"].toInt();
+    const Rows dy = grad_rows(grads[0]);
+    const int64_t M = dy.rows, K = dy.cols, F = ctx->saved_data["F"].toInt();
+    size_t nk, nf, nb;
+    check(fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
+    const Tensor scratch = space(nb, dy.t);
+    Tensor dX, dWgu, dWd;
+    if (flags & FP8_BLOCK_NEED_DX) dX = make(grads[0].sizes(), dy.t);
+    if (flags & FP8_BLOCK_NEED_DW) dWgu = make({K, 2 * F}, dy.t);
+    if (flags & FP8_BLOCK_NEED_DW2) dWd = make({F, K}, dy.t);
+    check(fp8_block_mlp_bwd(dy.p(), dy.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dWgu), ptr(dWd),
+                            stream_of(dy.t)),
+          "fp8_block_mlp_bwd");
+    return once(grads[0], {dX, dWgu, dWd});
+  }
+};
+
+}  // namespace
+
+PYBIND11_MODULE(_block_autograd, m) {
+  m.def("linear", [](const Tensor& X, const Tensor& W) { return Linear::apply(X, W); });
+  m.def("swiglu", [](const Tensor& gate, const Tensor& up) { return Swiglu::apply(gate, up); });
+  m.def("mlp", [](const Tensor& X, const Tensor& Wgu, const Tensor& Wd) { return Mlp::apply(X, Wgu, Wd); });
+}
