@@ -1,7 +1,7 @@
 """Block-scaled FP8: a power-of-two scale for each block of 128 elements.
 
 Python binding of the block entry points of include/fp8lin.h, and their
-autograd forms (compiled nodes, csrc/block_autograd.cpp):
+autograd forms (compiled: csrc/block_binding.cpp):
 
   fp8_block_quantize / fp8_block_dequantize   8-bit store and restore
   fp8_block_gemm                              product of two stored matrices
@@ -78,6 +78,11 @@ def _same_device(a: torch.Tensor, b: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be on {a.device}, got {b.device}")
 
 
+def _check_stored(q: "BlockTensor", name: str) -> None:
+    if not q.data.is_cuda:
+        raise ValueError(f"{name} must be on the device (no CPU path exists)")
+
+
 class BlockTensor:
     """A stored matrix [rows, cols] of an FP8 format: data (uint8) holds the
     codes, [rows, cols rounded up to 128], then the scales in the library's
@@ -137,41 +142,31 @@ def fp8_block_quantize(x: torch.Tensor, fmt="e4m3", rowwise: bool = True, transp
     """The stored form of a bf16 matrix x [rows, cols], blocks along its rows
     (rowwise), and of its transpose [cols, rows], blocks down the columns
     (transposed), from one read. Returns (BlockTensor or None, BlockTensor or None)."""
-    p, ld = _rows(x, "x")
+    _rows(x, "x")
     rows, cols = x.shape
     f = _fmt(fmt)
     if not rowwise and not transposed:
         raise ValueError("neither form is wanted")
-    q = qt = c = s = ct = st = None
-    if rowwise:
-        q = BlockTensor.empty(rows, cols, f, x.device)
-        c, s = q.pointers()
-    if transposed:
-        qt = BlockTensor.empty(cols, rows, f, x.device)
-        ct, st = qt.pointers()
-    check(load().fp8_block_quantize(p, rows, cols, ld, f, c, s, ct, st, _on(x)), "fp8_block_quantize")
-    return q, qt
+    q, qt = _binding().quantize(x, f, rowwise, transposed)
+    return (None if q is None else BlockTensor(q, rows, cols, f), None if qt is None else BlockTensor(qt, cols, rows, f))
 
 
 def fp8_block_dequantize(q: BlockTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a stored matrix, bf16 [rows, cols]; out: any row pitch."""
-    if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=_BF16, device=q.data.device)
-        p, ld = out.data_ptr(), q.cols
-    else:
+    _check_stored(q, "q")
+    if out is not None:
         if tuple(out.shape) != (q.rows, q.cols):
             raise ValueError("out has the wrong shape")
-        p, ld = _rows(out, "out")
+        _rows(out, "out")
         _same_device(q.data, out, "out")
-    c, s = q.pointers()
-    check(load().fp8_block_dequantize(c, s, q.rows, q.cols, q.fmt, p, ld, _on(out)), "fp8_block_dequantize")
-    return out
+    return _binding().dequantize(q.data, q.rows, q.cols, q.fmt, out)
 
 
 def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C [M, N] (bf16) = A B^T of stored A [M, R] and B [N, R], any formats."""
     if a.cols != b.cols:
         raise ValueError(f"reduction mismatch: A {a.shape}, B {b.shape}")
+    _check_stored(a, "A")
     _same_device(a.data, b.data, "B")
     M, N, R = a.rows, b.rows, a.cols
     if out is None:
@@ -193,12 +188,6 @@ def _gemm_bytes(M: int, N: int, R: int) -> int:
     return load().fp8_block_gemm_workspace_bytes(M, N, R)
 
 
-@functools.lru_cache(maxsize=4096)
-def _cached_bytes(M: int, K: int, N: int) -> int:
-    """Scratch of the serving linear; 0: the form for few rows, which takes none."""
-    return 0 if load().fp8_block_linear_few(M, K, N) else load().fp8_block_linear_cached_bytes(M, K, N)
-
-
 def _space(n: int, device) -> torch.Tensor:
     return torch.empty(n, dtype=_U8, device=device)
 
@@ -208,15 +197,15 @@ def _wants_grad(*tensors) -> bool:
 
 
 @functools.lru_cache(maxsize=None)
-def _autograd():
-    """The compiled autograd nodes (csrc/block_autograd.cpp)."""
+def _binding():
+    """The compiled binding (csrc/block_binding.cpp)."""
     load()
     try:
-        from . import _block_autograd
+        from . import _block_binding
     except ImportError as e:
-        raise ImportError("the block-scaled operators' autograd nodes are not built; build them with "
+        raise ImportError("the block-scaled operators' binding is not built; build it with "
                           f"`python -m tensor_scaled_fp8_amd.build` ({e})") from e
-    return _block_autograd
+    return _block_binding
 
 
 @functools.lru_cache(maxsize=4096)
@@ -237,7 +226,7 @@ def block_linear(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     if _wants_grad(X, W):
         _check_bf16(X, "X")
         _check_bf16(W, "W")
-        return _autograd().linear(X, W)
+        return _binding().linear(X, W)
     X2, px, ldx, M, K = _as_rows(X, "X")
     W2, pw, ldw, _, N = _as_rows(W, "W")
     n = _forward_bytes("fp8_block_linear_bytes", M, K, N)
@@ -267,25 +256,16 @@ def prepare_block_weight(W: torch.Tensor) -> BlockTensor:
 
 def fp8_block_linear_fwd_cached(X: torch.Tensor, w: BlockTensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [M, N] = X [M, K] W from a stored weight (prepare_block_weight)."""
-    p, ld = _rows(X, "X")
+    _rows(X, "X")
     M, K = X.shape
     N = w.rows
     if w.cols != K or w.fmt != 0:
         raise ValueError(f"X {tuple(X.shape)} does not go with the stored weight {w.shape} (E4M3, transposed)")
     _same_device(X, w.data, "w")
-    if Y is None:
-        Y = torch.empty((M, N), dtype=_BF16, device=X.device)
-    elif tuple(Y.shape) != (M, N) or Y.dtype is not _BF16 or not Y.is_contiguous() or Y.device != X.device:
+    if Y is not None and (tuple(Y.shape) != (M, N) or Y.dtype is not _BF16 or not Y.is_contiguous() or
+                          Y.device != X.device):
         raise ValueError("Y must be a contiguous bf16 [M, N] on X's device")
-    nb = _cached_bytes(M, K, N)
-    c, s = w.pointers()
-    if not nb:
-        check(load().fp8_block_linear_fwd_few(p, ld, M, K, N, c, s, Y.data_ptr(), _on(X)), "fp8_block_linear_fwd_few")
-        return Y
-    scratch = _space(nb, X.device)
-    check(load().fp8_block_linear_fwd_cached(p, ld, M, K, N, c, s, scratch.data_ptr(), nb, Y.data_ptr(), _on(X)),
-          "fp8_block_linear_fwd_cached")
-    return Y
+    return _binding().serve(X, w.data, N, Y)
 
 
 class BlockInferenceLinear(torch.nn.Module):
@@ -311,7 +291,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     if _wants_grad(gate, up):
         _check_bf16(gate, "gate")
         _check_bf16(up, "up")
-        return _autograd().swiglu(gate, up)
+        return _binding().swiglu(gate, up)
     g2, pg, ldg, rows, cols = _as_rows(gate, "gate")
     u2, pu, ldu, _, _ = _as_rows(up, "up")
     h = torch.empty(gate.shape, dtype=_BF16, device=gate.device)
@@ -331,7 +311,7 @@ def block_mlp(X: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor) -> torch.Ten
     if _wants_grad(X, Wgu, Wd):
         for t, name in ((X, "X"), (Wgu, "Wgu"), (Wd, "Wd")):
             _check_bf16(t, name)
-        return _autograd().mlp(X, Wgu, Wd)
+        return _binding().mlp(X, Wgu, Wd)
     X2, px, ldx, M, K = _as_rows(X, "X")
     G2, pg, ldg, _, _ = _as_rows(Wgu, "Wgu")
     D2, pd, ldd, F, _ = _as_rows(Wd, "Wd")

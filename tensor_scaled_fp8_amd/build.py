@@ -1,5 +1,5 @@
-"""Build libfp8lin.so (all HIP sources, gfx950 only) and the autograd nodes
-of the block-scaled operators (_block_autograd.so, host code against torch)
+"""Build libfp8lin.so (all HIP sources, gfx950 only) and the compiled binding
+of the block-scaled operators (_block_binding.so, host code against torch)
 in-tree.
 
     python -m tensor_scaled_fp8_amd.build [--jobs N]
@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8lin.so")
-AUTOGRAD = os.path.join(PKG, "_block_autograd.so")
+BINDING = os.path.join(PKG, "_block_binding.so")
 SOURCES = ["api.hip", "amax.hip", "cast.hip", "gemm.hip", "adam.hip", "block_quant.hip", "block_swiglu.hip",
            "block_gemm.hip", "block_serve.hip", "block_api.hip"]
 ARCH = "gfx950"
@@ -44,38 +44,38 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_autograd() -> str:
-    """block_autograd.cpp to an object, with the C++ ABI that torch was built with."""
+def _compile_binding() -> str:
+    """block_binding.cpp to an object, with the C++ ABI that torch was built with."""
     import torch
     from torch.utils.cpp_extension import include_paths
-    obj = os.path.join(BUILD_DIR, "block_autograd.o")
+    obj = os.path.join(BUILD_DIR, "block_binding.o")
     inc = [*include_paths(), "/opt/rocm/include", INCLUDE, sysconfig.get_paths()["include"]]
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{p}" for p in inc],
-           "-c", os.path.join(CSRC, "block_autograd.cpp"), "-o", obj]
+           "-c", os.path.join(CSRC, "block_binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{CXX} failed for block_autograd.cpp:\n{r.stderr}")
+        raise RuntimeError(f"{CXX} failed for block_binding.cpp:\n{r.stderr}")
     return obj
 
 
-def _link_autograd(obj: str) -> None:
+def _link_binding(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = AUTOGRAD + ".tmp"
+    tmp = BINDING + ".tmp"
     cmd = [CXX, "-shared", obj, "-o", tmp, f"-L{lib}", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip",
            f"-L{OUT_DIR}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN/lib", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link of the autograd nodes failed:\n{r.stderr}")
-    os.replace(tmp, AUTOGRAD)
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(jobs: int = 4, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        nodes = ex.submit(_compile_autograd)
+        nodes = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
         nodes = nodes.result()
     tmp = LIB + ".tmp"
@@ -84,9 +84,9 @@ def build(jobs: int = 4, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_autograd(nodes)
+    _link_binding(nodes)
     if verbose:
-        print(f"built {LIB} and {AUTOGRAD}")
+        print(f"built {LIB} and {BINDING}")
     return LIB
 
 

@@ -1,11 +1,14 @@
-// Autograd nodes of the block-scaled operators: argument layout, memory and
-// one C-ABI call each way. A backward runs on autograd's device thread; as
-// Python there it took 40 us a call more than an empty one where that thread
-// ran on another part of the chip than the caller's, since every object it
-// touches then moves between their caches.
+// The block-scaled operators' autograd nodes and their calls of few
+// microseconds (store, restore, serve): argument layout, memory and one
+// C-ABI call each. A backward runs on autograd's device thread; as Python
+// there it took 40 us a call more than an empty one where that thread ran on
+// another part of the chip than the caller's, since every object it touches
+// then moves between their caches.
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
+
+#include <optional>
 
 #include "fp8lin.h"
 
@@ -157,9 +160,62 @@ struct Mlp : torch::autograd::Function<Mlp> {
   }
 };
 
+// A stored matrix in one allocation: codes, then scales.
+int64_t round_blk(int64_t n) { return (n + 127) / 128 * 128; }
+struct Stored {
+  Tensor data;
+  uint8_t *codes, *scales;
+  Stored(const Tensor& d, int64_t rows, int64_t cols)
+      : data(d), codes((uint8_t*)data.data_ptr()), scales(codes + rows * round_blk(cols)) {}
+  Stored(int64_t rows, int64_t cols, const Tensor& like)
+      : Stored(space(rows * round_blk(cols) + round_blk(rows) * (round_blk(cols) / 128), like), rows, cols) {}
+};
+
+using Maybe = std::optional<Tensor>;
+
+std::pair<Maybe, Maybe> quantize(const Tensor& x, int64_t fmt, bool rowwise, bool transposed) {
+  const int64_t rows = x.size(0), cols = x.size(1);
+  std::optional<Stored> q, t;
+  if (rowwise) q.emplace(rows, cols, x);
+  if (transposed) t.emplace(cols, rows, x);
+  check(fp8_block_quantize(x.data_ptr(), rows, cols, x.stride(0), (fp8_fmt)fmt, q ? q->codes : nullptr,
+                           q ? q->scales : nullptr, t ? t->codes : nullptr, t ? t->scales : nullptr, stream_of(x)),
+        "fp8_block_quantize");
+  return {q ? Maybe(q->data) : Maybe(), t ? Maybe(t->data) : Maybe()};
+}
+
+Tensor dequantize(const Tensor& data, int64_t rows, int64_t cols, int64_t fmt, const Maybe& out) {
+  const Stored q(data, rows, cols);
+  const Tensor o = out ? *out : make({rows, cols}, data);
+  check(fp8_block_dequantize(q.codes, q.scales, rows, cols, (fp8_fmt)fmt, o.data_ptr(), o.stride(0), stream_of(o)),
+        "fp8_block_dequantize");
+  return o;
+}
+
+// Y [M, N] = X W for a stored weight (transposed form, [N, K])
+Tensor serve(const Tensor& X, const Tensor& weight, int64_t N, const Maybe& out) {
+  const int64_t M = X.size(0), K = X.size(1);
+  const Stored w(weight, N, K);
+  const Tensor Y = out ? *out : make({M, N}, X);
+  if (fp8_block_linear_few(M, K, N)) {
+    check(fp8_block_linear_fwd_few(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, Y.data_ptr(), stream_of(X)),
+          "fp8_block_linear_fwd_few");
+    return Y;
+  }
+  const size_t n = fp8_block_linear_cached_bytes(M, K, N);
+  const Tensor scratch = space(n, X);
+  check(fp8_block_linear_fwd_cached(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, ptr(scratch), n, Y.data_ptr(),
+                                    stream_of(X)),
+        "fp8_block_linear_fwd_cached");
+  return Y;
+}
+
 }  // namespace
 
-PYBIND11_MODULE(_block_autograd, m) {
+PYBIND11_MODULE(_block_binding, m) {
+  m.def("quantize", &quantize);
+  m.def("dequantize", &dequantize);
+  m.def("serve", &serve);
   m.def("linear", [](const Tensor& X, const Tensor& W) { return Linear::apply(X, W); });
   m.def("swiglu", [](const Tensor& gate, const Tensor& up) { return Swiglu::apply(gate, up); });
   m.def("mlp", [](const Tensor& X, const Tensor& Wgu, const Tensor& Wd) { return Mlp::apply(X, Wgu, Wd); });

@@ -1,6 +1,8 @@
 """Host-side checks of the serving linear for few rows (no GPU, no launch)."""
 import ctypes
 
+import pytest
+
 import tensor_scaled_fp8_amd as tsf
 from tensor_scaled_fp8_amd import _lib
 
@@ -25,3 +27,11 @@ def test_few_refusals():
         args = list(ok)
         args[at] = bad
         assert f(*args) == want, (at, bad)
+
+
+def test_stored_on_the_host_is_refused():
+    q = tsf.BlockTensor.empty(4, 8, "e4m3", "cpu")
+    with pytest.raises(ValueError, match="on the device"):
+        q.dequantize()
+    with pytest.raises(ValueError, match="on the device"):
+        tsf.fp8_block_gemm(q, q)
