@@ -47,10 +47,13 @@ Tensor space(size_t n, const Tensor& like) { return at::empty({(int64_t)n}, like
 Tensor make(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kBFloat16)); }
 void* ptr(const Tensor& t) { return t.defined() && t.numel() ? t.data_ptr() : nullptr; }
 
-// A graph of the gradients themselves (create_graph) is refused when it is
-// used: the kernels' results would be taken for constants.
-tensor_list once(const Tensor& dy, tensor_list out) {
-  if (!at::GradMode::is_enabled() || !dy.requires_grad()) return out;
+// A graph of the gradients themselves (create_graph, which is when a backward
+// runs with gradients enabled) is refused when it is used: the kernels'
+// results would be taken for constants. Whether the incoming gradient wants
+// one does not matter (a sum's is an expanded constant): the results depend on
+// the forward's operands too, and some of those do, or there would be no node.
+tensor_list once(tensor_list out) {
+  if (!at::GradMode::is_enabled()) return out;
   for (Tensor& t : out)
     if (t.defined()) t = t.detach().set_requires_grad(true);
   auto err = std::make_shared<torch::autograd::DelayedError>(
@@ -95,7 +98,7 @@ struct Linear : torch::autograd::Function<Linear> {
     check(fp8_block_linear_bwd(dy.p(), dy.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dW),
                                stream_of(dy.t)),
           "fp8_block_linear_bwd");
-    return once(grads[0], {dX, dW});
+    return once({dX, dW});
   }
 };
 
@@ -120,7 +123,7 @@ struct Swiglu : torch::autograd::Function<Swiglu> {
     if (need & 2) du = make(grads[0].sizes(), d.t);
     check(fp8_swiglu_bwd(d.p(), d.ld, d.rows, d.cols, ptr(kept), (size_t)kept.numel(), ptr(dg), ptr(du), stream_of(d.t)),
           "fp8_swiglu_bwd");
-    return once(grads[0], {dg, du});
+    return once({dg, du});
   }
 };
 
@@ -156,7 +159,7 @@ struct Mlp : torch::autograd::Function<Mlp> {
     check(fp8_block_mlp_bwd(dy.p(), dy.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dWgu), ptr(dWd),
                             stream_of(dy.t)),
           "fp8_block_mlp_bwd");
-    return once(grads[0], {dX, dWgu, dWd});
+    return once({dX, dWgu, dWd});
   }
 };
 
