@@ -12,8 +12,10 @@ autograd forms (compiled: csrc/block_binding.cpp):
   block_mlp, BlockMLP                         a SwiGLU MLP of all of these
 
 Matrices are bf16 on the device. Rows must be contiguous, with any pitch
-and alignment; the autograd forms copy other strides first. Work runs on
-the current stream of the tensors' device."""
+and alignment; the autograd forms copy other strides first. Their
+derivatives are first-order and reverse-mode: a gradient of a gradient and
+forward-mode tangents are refused. Work runs on the current stream of the
+tensors' device."""
 from __future__ import annotations
 
 import ctypes
@@ -21,6 +23,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import check, load
 from .binding import _fmt, _stream
@@ -193,6 +196,9 @@ def _space(n: int, device) -> torch.Tensor:
 
 
 def _wants_grad(*tensors) -> bool:
+    # a dual tensor wants no gradient by requires_grad, and its tangent would be left behind
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the block-scaled operators have no forward-mode derivatives")
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
