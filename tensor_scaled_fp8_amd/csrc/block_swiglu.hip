@@ -8,23 +8,56 @@
 // written once, the maxima of a block taken in registers. 4096 x 28672:
 // forward and backward 147 us each, 6.4 TB/s; the gradients of 2048 x 10240
 // straight to their stored forms 57 us, 3.3 TB/s (two waves a SIMD).
+#include <type_traits>
+
 #include "block_quant.h"
 
 namespace fp8lin {
 namespace {
 
-// v_exp and v_rcp are within 1 ulp or so of 32 bits, far below the
-// outputs' 8 bits; exp overflows to inf for g < -88, whose reciprocal is
-// the right 0
-__device__ inline float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+// s = 1 / (1 + e^-g), as s r^2. The exponential's argument is rounded in 32
+// bits, so s is off by about |g| 2^-23 relative, below the outputs' 8 bits
+// wherever s is not 0. Far below 0 the plain expression leaves 32 bits (1 / e^-g
+// is below 2^-126 from g = -87.4 on, e^-g above 2^128 from -88.8) where g s u is
+// still an ordinary number for a large u: there (FAR) s is taken at -80 and
+// the rest of e^g is the square of r, multiplied in last. Beyond g = -400 every
+// finite product is 0; the bound on g keeps the products before r finite.
+constexpr float kFar = -80.0f, kGone = -400.0f;
+struct Sigmoid {
+  float g, s, r;
+};
+template <bool FAR>
+__device__ inline Sigmoid sigmoid(float g) {
+  if constexpr (!FAR) return {g, __builtin_amdgcn_rcpf(1.0f + __expf(-g)), 1.0f};
+  const float c = g < kGone && g > -__builtin_inff() ? kGone : g;
+  return {c, __builtin_amdgcn_rcpf(1.0f + __expf(-fmaxf(c, kFar))),
+          __builtin_amdgcn_exp2f(fminf(c - kFar, 0.0f) * 0.72134752f)};  // log2(e) / 2
+}
+// f(far) for a row's 8 gates of each lane: far is whether any of the wave's is
+// below kFar, which is rare, so that the usual case pays for one branch
+template <typename F>
+__device__ inline void near_or_far(const float g[8], F&& f) {
+  const float lo = fminf(fminf(fminf(g[0], g[1]), fminf(g[2], g[3])), fminf(fminf(g[4], g[5]), fminf(g[6], g[7])));
+  if (__builtin_expect(__any(lo < kFar), 0)) f(std::true_type{});
+  else f(std::false_type{});
+}
 
+template <bool FAR>
+__device__ inline float gated(float g, float u) {
+  const Sigmoid q = sigmoid<FAR>(g);
+  const float h = q.g * q.s * u;
+  return FAR ? h * q.r * q.r : h;
+}
 struct Grads {
   float dg, du, h;
 };
+template <bool FAR>
 __device__ inline Grads grads(float g, float u, float dh) {
-  const float s = sigmoid(g);
-  const float gs = g * s;
-  return {dh * u * __builtin_fmaf(gs, 1.0f - s, s), dh * gs, gs * u};
+  const Sigmoid q = sigmoid<FAR>(g);
+  const float gs = q.g * q.s;
+  Grads x = {dh * u * __builtin_fmaf(gs, 1.0f - q.s, q.s), dh * gs, gs * u};
+  if constexpr (FAR) x = {x.dg * q.r * q.r, x.du * q.r * q.r, x.h * q.r * q.r};
+  return x;
 }
 
 template <int RPT>
@@ -43,8 +76,10 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(Bf16Mat gate, Bf16Mat u
     float g[8], u[8];
     widen8(wg[i], g);
     widen8(wu[i], u);
+    near_or_far(g, [&](auto far) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[i].f[k] = g[k] * sigmoid(g[k]) * u[k];
+      for (int k = 0; k < 8; ++k) y[i].f[k] = gated<decltype(far)::value>(g[k], u[k]);
+    });
     if (h && rr + 16 * i < gate.rows) store8(h + (rr + 16 * i) * ldh, cx, gate.cols, pack8(y[i].f));
   }
   auto put = [&](const BlockMat& o, const auto& v) {
@@ -96,12 +131,14 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(Bf16Mat dh, BlockMat gq
     widen8(wd[i], d);
     uncode8<FP8_E4M3>(wg[i], sg[i], g);
     uncode8<FP8_E4M3>(wu[i], su[i], u);
+    near_or_far(g, [&](auto far) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const Grads x = grads(g[k], u[k], d[k]);
-      a[k] = x.dg;
-      b[k] = x.du;
-    }
+      for (int k = 0; k < 8; ++k) {
+        const Grads x = grads<decltype(far)::value>(g[k], u[k], d[k]);
+        a[k] = x.dg;
+        b[k] = x.du;
+      }
+    });
     if (dg) store8(dg + r * lddg, cx, dh.cols, pack8(a));
     if (du) store8(du + r * lddu, cx, dh.cols, pack8(b));
   }
@@ -149,13 +186,15 @@ __global__ __launch_bounds__(512) void swiglu_bwd_quant_kernel(Bf16Mat dh, Block
     widen8(wd[i], d);
     uncode8<FP8_E4M3>(wg[i], sg[i], g);
     uncode8<FP8_E4M3>(wu[i], su[i], u);
+    near_or_far(g, [&](auto far) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const Grads x = grads(g[k], u[k], d[k]);
-      v[0][i].f[k] = x.h;
-      v[1][i].f[k] = x.dg;
-      v[2][i].f[k] = x.du;
-    }
+      for (int k = 0; k < 8; ++k) {
+        const Grads x = grads<decltype(far)::value>(g[k], u[k], d[k]);
+        v[0][i].f[k] = x.h;
+        v[1][i].f[k] = x.dg;
+        v[2][i].f[k] = x.du;
+      }
+    });
   }
   if (dgq.codes) {
     auto put = [&](const BlockMat& o, const Row8 (&x)[4]) {
