@@ -33,8 +33,29 @@ def _fmt(f) -> int:
         raise ValueError(f"unknown FP8 format {f!r}") from None
 
 
+# The stream's handle alone: a Stream object around it costs 2 us a call, as
+# much as a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch.cuda.current_stream(t.device).cuda_stream if _raw_stream is None else _raw_stream(t.get_device())
+
+
+def _at(t: torch.Tensor, f, *args):
+    """f(*args) with t's device current: a launch goes to the current device,
+    whose default stream is what a default stream's null handle stands for."""
+    device = t.get_device()
+    if device == _current_device():
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
+
+
+def _launch(t: torch.Tensor, entry: str, *args) -> None:
+    """An entry point on t's device and the current stream of that device."""
+    check(_at(t, getattr(load(), entry), *args, _stream(t)), entry)
 
 
 def _dev(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
@@ -67,22 +88,20 @@ def read_scale(s: torch.Tensor) -> dict:
 
 def fp8_scale_reset(s: torch.Tensor) -> None:
     n = s.numel() // SCALE_WORDS
-    check(load().fp8_scale_reset(_dev(s, torch.int32, "s"), n, _stream(s)), "fp8_scale_reset")
+    _launch(s, "fp8_scale_reset", _dev(s, torch.int32, "s"), n)
 
 
 def fp8_amax(x: torch.Tensor, s: torch.Tensor) -> None:
-    check(load().fp8_amax(_dev(x, torch.bfloat16, "x"), x.numel(), _dev(s, torch.int32, "s"),
-                          _stream(x)), "fp8_amax")
+    _launch(x, "fp8_amax", _dev(x, torch.bfloat16, "x"), x.numel(), _dev(s, torch.int32, "s"))
 
 
 def fp8_scale(fmt, s: torch.Tensor, margin: int = 0, mu_log2: int = 0) -> None:
-    check(load().fp8_scale(_fmt(fmt), margin, mu_log2, _dev(s, torch.int32, "s"), _stream(s)),
-          "fp8_scale")
+    _launch(s, "fp8_scale", _fmt(fmt), margin, mu_log2, _dev(s, torch.int32, "s"))
 
 
 def fp8_amax_scale(x: torch.Tensor, fmt, s: torch.Tensor, margin: int = 0, mu_log2: int = 0) -> None:
-    check(load().fp8_amax_scale(_dev(x, torch.bfloat16, "x"), x.numel(), _fmt(fmt), margin, mu_log2,
-                                _dev(s, torch.int32, "s"), _stream(x)), "fp8_amax_scale")
+    _launch(x, "fp8_amax_scale", _dev(x, torch.bfloat16, "x"), x.numel(), _fmt(fmt), margin, mu_log2,
+            _dev(s, torch.int32, "s"))
 
 
 def fp8_bias_host(amax: float, fmt, margin: int = 0, mu_log2: int = 0):
@@ -93,7 +112,7 @@ def fp8_bias_host(amax: float, fmt, margin: int = 0, mu_log2: int = 0):
 
 def fp8_scale_fixed(s: torch.Tensor, bias: int) -> None:
     """FP8-CSCALE: set the record to a constant bias (scale 2^bias)."""
-    check(load().fp8_scale_fixed(_dev(s, torch.int32, "s"), int(bias), _stream(s)), "fp8_scale_fixed")
+    _launch(s, "fp8_scale_fixed", _dev(s, torch.int32, "s"), int(bias))
 
 
 def fp8_cast(x: torch.Tensor, fmt, s: torch.Tensor, out_row: Optional[torch.Tensor] = None,
@@ -107,9 +126,8 @@ def fp8_cast(x: torch.Tensor, fmt, s: torch.Tensor, out_row: Optional[torch.Tens
         out_row = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     if transposed and out_t is None:
         out_t = torch.empty((cols, rows), dtype=torch.uint8, device=x.device)
-    check(load().fp8_cast(_dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), _dev(s, torch.int32, "s"),
-                          _dev(out_row, torch.uint8, "out_row"), _dev(out_t, torch.uint8, "out_t"),
-                          _stream(x)), "fp8_cast")
+    _launch(x, "fp8_cast", _dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), _dev(s, torch.int32, "s"),
+            _dev(out_row, torch.uint8, "out_row"), _dev(out_t, torch.uint8, "out_t"))
     return out_row, out_t
 
 
@@ -125,9 +143,8 @@ def fp8_quantize(x: torch.Tensor, fmt, s: torch.Tensor, margin: int = 0, mu_log2
         out_row = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     if transposed and out_t is None:
         out_t = torch.empty((cols, rows), dtype=torch.uint8, device=x.device)
-    check(load().fp8_quantize(_dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), margin, mu_log2,
-                              _dev(s, torch.int32, "s"), _dev(out_row, torch.uint8, "out_row"),
-                              _dev(out_t, torch.uint8, "out_t"), _stream(x)), "fp8_quantize")
+    _launch(x, "fp8_quantize", _dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), margin, mu_log2,
+            _dev(s, torch.int32, "s"), _dev(out_row, torch.uint8, "out_row"), _dev(out_t, torch.uint8, "out_t"))
     return out_row, out_t
 
 
@@ -141,9 +158,8 @@ def fp8_quantize_spec(x: torch.Tensor, fmt, s: torch.Tensor, margin: int = 0, mu
     rows, cols = x.shape
     if out_row is None:
         out_row = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    check(load().fp8_quantize_spec(_dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), margin, mu_log2,
-                                   _dev(s, torch.int32, "s"), _dev(out_row, torch.uint8, "out_row"), _stream(x)),
-          "fp8_quantize_spec")
+    _launch(x, "fp8_quantize_spec", _dev(x, torch.bfloat16, "x"), rows, cols, _fmt(fmt), margin, mu_log2,
+            _dev(s, torch.int32, "s"), _dev(out_row, torch.uint8, "out_row"))
     return out_row
 
 
@@ -172,7 +188,7 @@ def fp8_quantize_batch(tensors):
                                d.get("mu_log2", 0), _dev(d["s"], torch.int32, "s"),
                                _dev(out_row, torch.uint8, "out_row"), _dev(out_t, torch.uint8, "out_t"))
         outs.append((out_row, out_t))
-    check(load().fp8_quantize_batch(args, n, _stream(tensors[0]["x"])), "fp8_quantize_batch")
+    _launch(tensors[0]["x"], "fp8_quantize_batch", args, n)
     return outs
 
 
@@ -187,9 +203,9 @@ def fp8_gemm_nt(a: torch.Tensor, fa, sa: torch.Tensor, b: torch.Tensor, fb, sb: 
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     if tuple(out.shape) != (M, N):
         raise ValueError("out has the wrong shape")
-    check(load().fp8_gemm_nt(_dev(a, torch.uint8, "A"), _fmt(fa), _dev(sa, torch.int32, "sa"),
-                             _dev(b, torch.uint8, "B"), _fmt(fb), _dev(sb, torch.int32, "sb"),
-                             M, N, R, _dev(out, torch.bfloat16, "out"), _stream(a)), "fp8_gemm_nt")
+    _launch(a, "fp8_gemm_nt", _dev(a, torch.uint8, "A"), _fmt(fa), _dev(sa, torch.int32, "sa"),
+            _dev(b, torch.uint8, "B"), _fmt(fb), _dev(sb, torch.int32, "sb"), M, N, R,
+            _dev(out, torch.bfloat16, "out"))
     return out
 
 
@@ -227,12 +243,10 @@ def fp8_gemm(a: torch.Tensor, fa, sa: torch.Tensor, b: torch.Tensor, fb, sb: tor
     split "auto", "never" or "tail")."""
     g, out = _gemm_args(a, fa, sa, b, fb, sb, out, a_layout, b_layout)
     if workspace is None:
-        check(load().fp8_gemm(g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C, _stream(a)),
-              "fp8_gemm")
+        _launch(a, "fp8_gemm", g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C)
     else:
-        check(load().fp8_gemm_ws(g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C, SPLITS[split],
-                                 _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(a)),
-              "fp8_gemm_ws")
+        _launch(a, "fp8_gemm_ws", g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C, SPLITS[split],
+                _dev(workspace, torch.uint8, "workspace"), workspace.numel())
     return out
 
 
@@ -248,8 +262,7 @@ def fp8_gemm_noalloc(a: torch.Tensor, fa, sa: torch.Tensor, b: torch.Tensor, fb,
     if out is None:
         raise ValueError("fp8_gemm_noalloc needs the output tensor")
     g, out = _gemm_args(a, fa, sa, b, fb, sb, out, a_layout, b_layout)
-    check(load().fp8_gemm_noalloc(g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C, SPLITS[split],
-                                  _stream(a)), "fp8_gemm_noalloc")
+    _launch(a, "fp8_gemm_noalloc", g.A, g.fa, g.la, g.sa, g.B, g.fb, g.lb, g.sb, g.M, g.N, g.R, g.C, SPLITS[split])
     return out
 
 
@@ -269,7 +282,7 @@ def fp8_gemm_pair(first: dict, second: dict):
                           d.get("a_layout", "rows"), d.get("b_layout", "rows"))
     g0, out0 = one(first)
     g1, out1 = one(second)
-    check(load().fp8_gemm_pair(ctypes.byref(g0), ctypes.byref(g1), _stream(first["a"])), "fp8_gemm_pair")
+    _launch(first["a"], "fp8_gemm_pair", ctypes.byref(g0), ctypes.byref(g1))
     return out0, out1
 
 
@@ -307,9 +320,8 @@ def fp8_linear_fwd(X: torch.Tensor, W: torch.Tensor, ws: LinearWorkspace, margin
         raise ValueError("shape mismatch between X, W and the workspace")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    check(load().fp8_linear_fwd(_dev(X, torch.bfloat16, "X"), _dev(W, torch.bfloat16, "W"), M, K, N,
-                                margin, ctypes.byref(ws.c), _dev(Y, torch.bfloat16, "Y"), _stream(X)),
-          "fp8_linear_fwd")
+    _launch(X, "fp8_linear_fwd", _dev(X, torch.bfloat16, "X"), _dev(W, torch.bfloat16, "W"), M, K, N, margin,
+            ctypes.byref(ws.c), _dev(Y, torch.bfloat16, "Y"))
     return Y
 
 
@@ -323,9 +335,8 @@ def fp8_linear_bwd(dY: torch.Tensor, ws: LinearWorkspace, margin: int = 0, mu_lo
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
     if need_dw and dW is None:
         dW = torch.empty((K, N), dtype=torch.bfloat16, device=dY.device)
-    check(load().fp8_linear_bwd(_dev(dY, torch.bfloat16, "dY"), M, K, N, margin, mu_log2,
-                                ctypes.byref(ws.c), _dev(dX, torch.bfloat16, "dX"),
-                                _dev(dW, torch.bfloat16, "dW"), _stream(dY)), "fp8_linear_bwd")
+    _launch(dY, "fp8_linear_bwd", _dev(dY, torch.bfloat16, "dY"), M, K, N, margin, mu_log2, ctypes.byref(ws.c),
+            _dev(dX, torch.bfloat16, "dX"), _dev(dW, torch.bfloat16, "dW"))
     return dX, dW
 
 
@@ -439,11 +450,10 @@ def fp8_wgrad_fp8(x8: torch.Tensor, sx: torch.Tensor, dy8: torch.Tensor, sdy: to
         dw8t = torch.empty((N, K), dtype=torch.uint8, device=dev)
     if s_dw is None:
         s_dw = new_scale(1, dev)[0]
-    check(load().fp8_wgrad_fp8(_dev(x8, torch.uint8, "x8"), LAYOUTS[x_layout], _dev(sx, torch.int32, "sx"),
-                               _dev(dy8, torch.uint8, "dy8"), LAYOUTS[dy_layout], _dev(sdy, torch.int32, "sdy"),
-                               K, N, M, margin, mu_log2, _dev(dW, torch.bfloat16, "dW"),
-                               _dev(s_dw, torch.int32, "s_dw"), _dev(dw8, torch.uint8, "dw8"),
-                               _dev(dw8t, torch.uint8, "dw8t"), _stream(x8)), "fp8_wgrad_fp8")
+    _launch(x8, "fp8_wgrad_fp8", _dev(x8, torch.uint8, "x8"), LAYOUTS[x_layout], _dev(sx, torch.int32, "sx"),
+            _dev(dy8, torch.uint8, "dy8"), LAYOUTS[dy_layout], _dev(sdy, torch.int32, "sdy"), K, N, M, margin,
+            mu_log2, _dev(dW, torch.bfloat16, "dW"), _dev(s_dw, torch.int32, "s_dw"), _dev(dw8, torch.uint8, "dw8"),
+            _dev(dw8t, torch.uint8, "dw8t"))
     return dW, dw8, dw8t, s_dw
 
 
@@ -489,10 +499,9 @@ def fp8_linear_fwd_cached(X: torch.Tensor, w8: torch.Tensor, sw: torch.Tensor, x
         raise ValueError(f"unknown x_scaling {x_scaling!r}") from None
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    check(load().fp8_linear_fwd_cached(_dev(X, torch.bfloat16, "X"), M, K, N, margin, mode,
-                                       _dev(w8, torch.uint8, "w8"), LAYOUTS[w_layout], _dev(sw, torch.int32, "sw"),
-                                       _dev(x8, torch.uint8, "x8"), _dev(sx, torch.int32, "sx"),
-                                       _dev(Y, torch.bfloat16, "Y"), _stream(X)), "fp8_linear_fwd_cached")
+    _launch(X, "fp8_linear_fwd_cached", _dev(X, torch.bfloat16, "X"), M, K, N, margin, mode,
+            _dev(w8, torch.uint8, "w8"), LAYOUTS[w_layout], _dev(sw, torch.int32, "sw"),
+            _dev(x8, torch.uint8, "x8"), _dev(sx, torch.int32, "sx"), _dev(Y, torch.bfloat16, "Y"))
     return Y
 
 
@@ -544,9 +553,8 @@ class AdamState:
 
 
 def fp8_adam_init_master(w_bf16: torch.Tensor, w16: torch.Tensor, s_w: torch.Tensor) -> None:
-    check(load().fp8_adam_init_master(w_bf16.numel(), _dev(w_bf16, torch.bfloat16, "w_bf16"),
-                                      _dev(w16, torch.int16, "w16"), _dev(s_w, torch.int32, "s_w"),
-                                      _stream(w_bf16)), "fp8_adam_init_master")
+    _launch(w_bf16, "fp8_adam_init_master", w_bf16.numel(), _dev(w_bf16, torch.bfloat16, "w_bf16"),
+            _dev(w16, torch.int16, "w16"), _dev(s_w, torch.int32, "s_w"))
 
 
 def fp8_adam_step(state: AdamState, g8: torch.Tensor, s_g: torch.Tensor, lr: float, beta1: float = 0.9,
@@ -558,12 +566,11 @@ def fp8_adam_step(state: AdamState, g8: torch.Tensor, s_g: torch.Tensor, lr: flo
     if g8.numel() != state.n:
         raise ValueError("gradient size differs from the state's")
     t = state.step_count + 1 if step is None else int(step)
-    check(load().fp8_adam_step(state.n, _dev(g8, torch.uint8, "g8"), _dev(s_g, torch.int32, "s_g"),
-                               _dev(state.m1, torch.uint8, "m1"), _dev(state.s_m1, torch.int32, "s_m1"),
-                               _dev(state.m2, torch.int16, "m2"), _dev(state.s_m2, torch.int32, "s_m2"),
-                               _dev(state.w16, torch.int16, "w16"), _dev(state.s_w, torch.int32, "s_w"),
-                               _dev(w_bf16, torch.bfloat16, "w_bf16"), lr, beta1, beta2, eps, weight_decay, t,
-                               _stream(g8)), "fp8_adam_step")
+    _launch(g8, "fp8_adam_step", state.n, _dev(g8, torch.uint8, "g8"), _dev(s_g, torch.int32, "s_g"),
+            _dev(state.m1, torch.uint8, "m1"), _dev(state.s_m1, torch.int32, "s_m1"),
+            _dev(state.m2, torch.int16, "m2"), _dev(state.s_m2, torch.int32, "s_m2"),
+            _dev(state.w16, torch.int16, "w16"), _dev(state.s_w, torch.int32, "s_w"),
+            _dev(w_bf16, torch.bfloat16, "w_bf16"), lr, beta1, beta2, eps, weight_decay, t)
     state.step_count = t
     return w_bf16
 
@@ -585,14 +592,13 @@ def fp8_adam_step_spec(state: AdamState, g8: torch.Tensor, s_g: torch.Tensor, lr
     if state.alt is None:
         state.alt = (torch.empty_like(state.m1), torch.empty_like(state.m2), torch.empty_like(state.w16))
     m1o, m2o, w16o = state.alt
-    check(load().fp8_adam_step_spec(state.n, _dev(g8, torch.uint8, "g8"), _dev(s_g, torch.int32, "s_g"),
-                                    _dev(state.m1, torch.uint8, "m1"), _dev(state.m2, torch.int16, "m2"),
-                                    _dev(state.w16, torch.int16, "w16"), _dev(m1o, torch.uint8, "m1_out"),
-                                    _dev(m2o, torch.int16, "m2_out"), _dev(w16o, torch.int16, "w16_out"),
-                                    _dev(state.s_m1, torch.int32, "s_m1"), _dev(state.s_m2, torch.int32, "s_m2"),
-                                    _dev(state.s_w, torch.int32, "s_w"), _dev(w_bf16, torch.bfloat16, "w_bf16"),
-                                    _dev(missed, torch.int32, "missed"), lr, beta1, beta2, eps, weight_decay, t,
-                                    _stream(g8)), "fp8_adam_step_spec")
+    _launch(g8, "fp8_adam_step_spec", state.n, _dev(g8, torch.uint8, "g8"), _dev(s_g, torch.int32, "s_g"),
+            _dev(state.m1, torch.uint8, "m1"), _dev(state.m2, torch.int16, "m2"),
+            _dev(state.w16, torch.int16, "w16"), _dev(m1o, torch.uint8, "m1_out"), _dev(m2o, torch.int16, "m2_out"),
+            _dev(w16o, torch.int16, "w16_out"), _dev(state.s_m1, torch.int32, "s_m1"),
+            _dev(state.s_m2, torch.int32, "s_m2"), _dev(state.s_w, torch.int32, "s_w"),
+            _dev(w_bf16, torch.bfloat16, "w_bf16"), _dev(missed, torch.int32, "missed"), lr, beta1, beta2, eps,
+            weight_decay, t)
     state.alt = (state.m1, state.m2, state.w16)
     state.m1, state.m2, state.w16 = m1o, m2o, w16o
     state.step_count = t

@@ -26,18 +26,10 @@ import torch
 from torch.autograd import forward_ad
 
 from ._lib import check, load
-from .binding import _fmt, _stream
+from .binding import _at, _fmt, _launch
 
 BLOCK = 128
 _BF16, _U8 = torch.bfloat16, torch.uint8
-
-# The stream's handle alone: a Stream object around it costs 2 us a call,
-# as much as a launch.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _on(t: torch.Tensor) -> int:
-    return _stream(t) if _raw_stream is None else _raw_stream(t.get_device())
 
 
 def _round(n: int) -> int:
@@ -150,7 +142,7 @@ def fp8_block_quantize(x: torch.Tensor, fmt="e4m3", rowwise: bool = True, transp
     f = _fmt(fmt)
     if not rowwise and not transposed:
         raise ValueError("neither form is wanted")
-    q, qt = _binding().quantize(x, f, rowwise, transposed)
+    q, qt = _at(x, _binding().quantize, x, f, rowwise, transposed)
     return (None if q is None else BlockTensor(q, rows, cols, f), None if qt is None else BlockTensor(qt, cols, rows, f))
 
 
@@ -162,7 +154,7 @@ def fp8_block_dequantize(q: BlockTensor, out: Optional[torch.Tensor] = None) -> 
             raise ValueError("out has the wrong shape")
         _rows(out, "out")
         _same_device(q.data, out, "out")
-    return _binding().dequantize(q.data, q.rows, q.cols, q.fmt, out)
+    return _at(q.data, _binding().dequantize, q.data, q.rows, q.cols, q.fmt, out)
 
 
 def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -180,8 +172,8 @@ def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] =
     _same_device(a.data, out, "out")
     nb = _gemm_bytes(M, N, R)
     ws = torch.empty(nb, dtype=_U8, device=a.device) if nb else None
-    check(load().fp8_block_gemm(*a.pointers(), a.fmt, *b.pointers(), b.fmt, M, N, R, p, ld,
-                                ws.data_ptr() if nb else None, nb, _on(out)), "fp8_block_gemm")
+    _launch(a.data, "fp8_block_gemm", *a.pointers(), a.fmt, *b.pointers(), b.fmt, M, N, R, p, ld,
+            ws.data_ptr() if nb else None, nb)
     return out
 
 
@@ -232,14 +224,13 @@ def block_linear(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     if _wants_grad(X, W):
         _check_bf16(X, "X")
         _check_bf16(W, "W")
-        return _binding().linear(X, W)
+        return _at(X, _binding().linear, X, W)
     X2, px, ldx, M, K = _as_rows(X, "X")
     W2, pw, ldw, _, N = _as_rows(W, "W")
     n = _forward_bytes("fp8_block_linear_bytes", M, K, N)
     scratch = _space(n, X.device)
     Y = torch.empty((*X.shape[:-1], N), dtype=_BF16, device=X.device)
-    check(load().fp8_block_linear_fwd(px, ldx, pw, ldw, M, K, N, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr(),
-                                      _on(X)), "fp8_block_linear_fwd")
+    _launch(X, "fp8_block_linear_fwd", px, ldx, pw, ldw, M, K, N, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr())
     return Y
 
 
@@ -271,7 +262,7 @@ def fp8_block_linear_fwd_cached(X: torch.Tensor, w: BlockTensor, Y: Optional[tor
     if Y is not None and (tuple(Y.shape) != (M, N) or Y.dtype is not _BF16 or not Y.is_contiguous() or
                           Y.device != X.device):
         raise ValueError("Y must be a contiguous bf16 [M, N] on X's device")
-    return _binding().serve(X, w.data, N, Y)
+    return _at(X, _binding().serve, X, w.data, N, Y)
 
 
 class BlockInferenceLinear(torch.nn.Module):
@@ -297,11 +288,11 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     if _wants_grad(gate, up):
         _check_bf16(gate, "gate")
         _check_bf16(up, "up")
-        return _binding().swiglu(gate, up)
+        return _at(gate, _binding().swiglu, gate, up)
     g2, pg, ldg, rows, cols = _as_rows(gate, "gate")
     u2, pu, ldu, _, _ = _as_rows(up, "up")
     h = torch.empty(gate.shape, dtype=_BF16, device=gate.device)
-    check(load().fp8_swiglu_fwd(pg, ldg, pu, ldu, rows, cols, h.data_ptr(), None, 0, _on(gate)), "fp8_swiglu_fwd")
+    _launch(gate, "fp8_swiglu_fwd", pg, ldg, pu, ldu, rows, cols, h.data_ptr(), None, 0)
     return h
 
 
@@ -317,15 +308,14 @@ def block_mlp(X: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor) -> torch.Ten
     if _wants_grad(X, Wgu, Wd):
         for t, name in ((X, "X"), (Wgu, "Wgu"), (Wd, "Wd")):
             _check_bf16(t, name)
-        return _binding().mlp(X, Wgu, Wd)
+        return _at(X, _binding().mlp, X, Wgu, Wd)
     X2, px, ldx, M, K = _as_rows(X, "X")
     G2, pg, ldg, _, _ = _as_rows(Wgu, "Wgu")
     D2, pd, ldd, F, _ = _as_rows(Wd, "Wd")
     n = _forward_bytes("fp8_block_mlp_bytes", M, K, F)
     scratch = _space(n, X.device)
     Y = torch.empty(X.shape, dtype=_BF16, device=X.device)
-    check(load().fp8_block_mlp_fwd(px, ldx, pg, ldg, pd, ldd, M, K, F, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr(),
-                                   _on(X)), "fp8_block_mlp_fwd")
+    _launch(X, "fp8_block_mlp_fwd", px, ldx, pg, ldg, pd, ldd, M, K, F, 0, None, 0, scratch.data_ptr(), n, Y.data_ptr())
     return Y
 
 
