@@ -73,7 +73,21 @@ def _same_device(a: torch.Tensor, b: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be on {a.device}, got {b.device}")
 
 
+def _stored_bytes(rows: int, cols: int) -> int:
+    pitch = _round(cols)
+    return rows * pitch + _round(rows) * (pitch // BLOCK)
+
+
+def _check_data(data: torch.Tensor, rows: int, cols: int, name: str) -> None:
+    if rows < 0 or cols < 0:
+        raise ValueError(f"{name}: negative size [{rows}, {cols}]")
+    if data.dtype is not _U8 or data.dim() != 1 or not data.is_contiguous() or data.numel() != _stored_bytes(rows, cols):
+        raise ValueError(f"{name} must be {_stored_bytes(rows, cols)} contiguous bytes (uint8, 1-D) for "
+                         f"[{rows}, {cols}], got {data.dtype} {tuple(data.shape)}")
+
+
 def _check_stored(q: "BlockTensor", name: str) -> None:
+    _check_data(q.data, q.rows, q.cols, name)
     if not q.data.is_cuda:
         raise ValueError(f"{name} must be on the device (no CPU path exists)")
 
@@ -85,14 +99,20 @@ class BlockTensor:
 
     __slots__ = ("data", "rows", "cols", "fmt")
 
-    def __init__(self, data: torch.Tensor, rows: int, cols: int, fmt: int):
-        self.data, self.rows, self.cols, self.fmt = data, rows, cols, fmt
+    def __init__(self, data: torch.Tensor, rows: int, cols: int, fmt):
+        _check_data(data, rows, cols, "data")
+        self.data, self.rows, self.cols, self.fmt = data, rows, cols, _fmt(fmt)
 
     @classmethod
     def empty(cls, rows: int, cols: int, fmt, device) -> "BlockTensor":
-        pitch = _round(cols)
-        return cls(torch.empty(rows * pitch + _round(rows) * (pitch // BLOCK), dtype=_U8, device=device), rows, cols,
-                   _fmt(fmt))
+        return cls(torch.empty(_stored_bytes(rows, cols), dtype=_U8, device=device), rows, cols, fmt)
+
+    @classmethod
+    def _made(cls, data: torch.Tensor, rows: int, cols: int, fmt: int) -> "BlockTensor":
+        """Of data that was allocated for it: nothing to check."""
+        q = cls.__new__(cls)
+        q.data, q.rows, q.cols, q.fmt = data, rows, cols, fmt
+        return q
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -143,12 +163,14 @@ def fp8_block_quantize(x: torch.Tensor, fmt="e4m3", rowwise: bool = True, transp
     if not rowwise and not transposed:
         raise ValueError("neither form is wanted")
     q, qt = _at(x, _binding().quantize, x, f, rowwise, transposed)
-    return (None if q is None else BlockTensor(q, rows, cols, f), None if qt is None else BlockTensor(qt, cols, rows, f))
+    return (None if q is None else BlockTensor._made(q, rows, cols, f),
+            None if qt is None else BlockTensor._made(qt, cols, rows, f))
 
 
 def fp8_block_dequantize(q: BlockTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a stored matrix, bf16 [rows, cols]; out: any row pitch."""
-    _check_stored(q, "q")
+    if not q.data.is_cuda:
+        raise ValueError("q must be on the device (no CPU path exists)")
     if out is not None:
         if tuple(out.shape) != (q.rows, q.cols):
             raise ValueError("out has the wrong shape")
@@ -162,6 +184,7 @@ def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] =
     if a.cols != b.cols:
         raise ValueError(f"reduction mismatch: A {a.shape}, B {b.shape}")
     _check_stored(a, "A")
+    _check_data(b.data, b.rows, b.cols, "B")
     _same_device(a.data, b.data, "B")
     M, N, R = a.rows, b.rows, a.cols
     if out is None:

@@ -14,6 +14,7 @@
 
 namespace {
 
+namespace py = pybind11;
 using at::Tensor;
 using torch::autograd::AutogradContext;
 using torch::autograd::tensor_list;
@@ -168,10 +169,19 @@ int64_t round_blk(int64_t n) { return (n + 127) / 128 * 128; }
 struct Stored {
   Tensor data;
   uint8_t *codes, *scales;
-  Stored(const Tensor& d, int64_t rows, int64_t cols)
-      : data(d), codes((uint8_t*)data.data_ptr()), scales(codes + rows * round_blk(cols)) {}
-  Stored(int64_t rows, int64_t cols, const Tensor& like)
-      : Stored(space(rows * round_blk(cols) + round_blk(rows) * (round_blk(cols) / 128), like), rows, cols) {}
+  static int64_t bytes(int64_t rows, int64_t cols) {
+    return rows * round_blk(cols) + round_blk(rows) * (round_blk(cols) / 128);
+  }
+  // the kernels read all of it: what is not that long is refused
+  Stored(const Tensor& d, int64_t rows, int64_t cols) : data(d) {
+    const int64_t n = rows < 0 || cols < 0 ? -1 : bytes(rows, cols);
+    if (data.numel() != n || data.scalar_type() != at::kByte || !data.is_contiguous())
+      throw py::value_error("a stored [" + std::to_string(rows) + ", " + std::to_string(cols) + "] must be " +
+                            std::to_string(n) + " contiguous bytes (uint8)");
+    codes = (uint8_t*)data.data_ptr();
+    scales = codes + rows * round_blk(cols);
+  }
+  Stored(int64_t rows, int64_t cols, const Tensor& like) : Stored(space(bytes(rows, cols), like), rows, cols) {}
 };
 
 using Maybe = std::optional<Tensor>;
