@@ -121,12 +121,15 @@ def load() -> ctypes.CDLL:
             f"libfp8lin.so not found at {LIB_PATH}; build it with "
             "`python -m tensor_scaled_fp8_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
+    if not hasattr(lib, "fp8_abi_version") or lib.fp8_abi_version() != ABI_VERSION:
+        found = lib.fp8_abi_version() if hasattr(lib, "fp8_abi_version") else "unknown"
+        raise ImportError(f"libfp8lin ABI {found} != expected {ABI_VERSION}")
     for name, (res, args) in SIGNATURES.items():
-        fn = getattr(lib, name)
+        fn = getattr(lib, name, None)
+        if fn is None:
+            raise ImportError(f"{LIB_PATH} lacks {name}; build it again with `python -m tensor_scaled_fp8_amd.build`")
         fn.restype = res
         fn.argtypes = args
-    if lib.fp8_abi_version() != ABI_VERSION:
-        raise ImportError(f"libfp8lin ABI {lib.fp8_abi_version()} != expected {ABI_VERSION}")
     _lib = lib
     return lib
 

@@ -63,8 +63,9 @@ def _link_binding(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
+    # not linked with the library: it takes the entry points of the one that is loaded
     cmd = [CXX, "-shared", obj, "-o", tmp, f"-L{lib}", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip",
-           f"-L{OUT_DIR}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN/lib", f"-Wl,-rpath,{lib}"]
+           "-ldl", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr}")

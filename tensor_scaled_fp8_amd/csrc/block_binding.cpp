@@ -5,6 +5,7 @@
 // another part of the chip than the caller's, since every object it touches
 // then moves between their caches.
 #include <c10/hip/HIPStream.h>
+#include <dlfcn.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
@@ -19,8 +20,30 @@ using at::Tensor;
 using torch::autograd::AutogradContext;
 using torch::autograd::tensor_list;
 
+// The entry points, of the library that the package has loaded (FP8LIN_LIB may
+// name another than the one beside this file: linked with that, one process
+// would compute with two).
+#define FP8LIN_ENTRIES(X) \
+  X(fp8_block_dequantize) X(fp8_block_linear_bwd) X(fp8_block_linear_bytes) X(fp8_block_linear_cached_bytes) \
+  X(fp8_block_linear_few) X(fp8_block_linear_fwd) X(fp8_block_linear_fwd_cached) X(fp8_block_linear_fwd_few) \
+  X(fp8_block_mlp_bwd) X(fp8_block_mlp_bytes) X(fp8_block_mlp_fwd) X(fp8_block_quantize) X(fp8_status_str) \
+  X(fp8_swiglu_bwd) X(fp8_swiglu_fwd) X(fp8_swiglu_kept_bytes)
+struct Api {
+#define X(name) decltype(&::name) name;
+  FP8LIN_ENTRIES(X)
+#undef X
+  void open(void* library) {
+#define X(entry)                                            \
+  entry = (decltype(entry))dlsym(library, #entry);          \
+  if (!entry) throw py::import_error("libfp8lin lacks " #entry);
+    FP8LIN_ENTRIES(X)
+#undef X
+  }
+};
+Api api;
+
 void check(fp8_status s, const char* what) {
-  if (s != FP8_OK) throw std::runtime_error(std::string(what) + ": " + fp8_status_str(s) + " (status " + std::to_string((int)s) + ")");
+  if (s != FP8_OK) throw std::runtime_error(std::string(what) + ": " + api.fp8_status_str(s) + " (status " + std::to_string((int)s) + ")");
 }
 hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.get_device()).stream(); }
 
@@ -70,12 +93,12 @@ struct Linear : torch::autograd::Function<Linear> {
     const Rows x(X), w(W);
     const int64_t M = x.rows, K = x.cols, N = w.cols;
     size_t nk, nf, nb;
-    check(fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
+    check(api.fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
     const Tensor kept = space(nk, X), scratch = space(nf, X);
     auto shape = X.sizes().vec();
     shape.back() = N;
     Tensor Y = make(shape, X);
-    check(fp8_block_linear_fwd(x.p(), x.ld, w.p(), w.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nf, Y.data_ptr(),
+    check(api.fp8_block_linear_fwd(x.p(), x.ld, w.p(), w.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nf, Y.data_ptr(),
                                stream_of(X)),
           "fp8_block_linear_fwd");
     ctx->save_for_backward({kept});
@@ -91,12 +114,12 @@ struct Linear : torch::autograd::Function<Linear> {
     const Rows dy = grad_rows(grads[0]);
     const int64_t M = dy.rows, K = shape.back(), N = ctx->saved_data["N"].toInt();
     size_t nk, nf, nb;
-    check(fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
+    check(api.fp8_block_linear_bytes(M, K, N, flags, &nk, &nf, &nb), "fp8_block_linear_bytes");
     const Tensor scratch = space(nb, dy.t);
     Tensor dX, dW;
     if (flags & FP8_BLOCK_NEED_DX) dX = make(shape, dy.t);
     if (flags & FP8_BLOCK_NEED_DW) dW = make({K, N}, dy.t);
-    check(fp8_block_linear_bwd(dy.p(), dy.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dW),
+    check(api.fp8_block_linear_bwd(dy.p(), dy.ld, M, K, N, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dW),
                                stream_of(dy.t)),
           "fp8_block_linear_bwd");
     return once({dX, dW});
@@ -106,10 +129,10 @@ struct Linear : torch::autograd::Function<Linear> {
 struct Swiglu : torch::autograd::Function<Swiglu> {
   static Tensor forward(AutogradContext* ctx, const Tensor& gate, const Tensor& up) {
     const Rows g(gate), u(up);
-    const size_t n = fp8_swiglu_kept_bytes(g.rows, g.cols);
+    const size_t n = api.fp8_swiglu_kept_bytes(g.rows, g.cols);
     const Tensor kept = space(n, gate);
     Tensor h = make(gate.sizes(), gate);
-    check(fp8_swiglu_fwd(g.p(), g.ld, u.p(), u.ld, g.rows, g.cols, h.data_ptr(), ptr(kept), n, stream_of(gate)),
+    check(api.fp8_swiglu_fwd(g.p(), g.ld, u.p(), u.ld, g.rows, g.cols, h.data_ptr(), ptr(kept), n, stream_of(gate)),
           "fp8_swiglu_fwd");
     ctx->save_for_backward({kept});
     ctx->saved_data["need"] = (int64_t)(flag(gate, 1) | flag(up, 2));
@@ -122,7 +145,7 @@ struct Swiglu : torch::autograd::Function<Swiglu> {
     Tensor dg, du;
     if (need & 1) dg = make(grads[0].sizes(), d.t);
     if (need & 2) du = make(grads[0].sizes(), d.t);
-    check(fp8_swiglu_bwd(d.p(), d.ld, d.rows, d.cols, ptr(kept), (size_t)kept.numel(), ptr(dg), ptr(du), stream_of(d.t)),
+    check(api.fp8_swiglu_bwd(d.p(), d.ld, d.rows, d.cols, ptr(kept), (size_t)kept.numel(), ptr(dg), ptr(du), stream_of(d.t)),
           "fp8_swiglu_bwd");
     return once({dg, du});
   }
@@ -134,10 +157,10 @@ struct Mlp : torch::autograd::Function<Mlp> {
     const Rows x(X), g(Wgu), d(Wd);
     const int64_t M = x.rows, K = x.cols, F = d.rows;
     size_t nk, nf, nb;
-    check(fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
+    check(api.fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
     const Tensor kept = space(nk, X), scratch = space(nf, X);
     Tensor Y = make(X.sizes(), X);
-    check(fp8_block_mlp_fwd(x.p(), x.ld, g.p(), g.ld, d.p(), d.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nf,
+    check(api.fp8_block_mlp_fwd(x.p(), x.ld, g.p(), g.ld, d.p(), d.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nf,
                             Y.data_ptr(), stream_of(X)),
           "fp8_block_mlp_fwd");
     ctx->save_for_backward({kept});
@@ -151,13 +174,13 @@ struct Mlp : torch::autograd::Function<Mlp> {
     const Rows dy = grad_rows(grads[0]);
     const int64_t M = dy.rows, K = dy.cols, F = ctx->saved_data["F"].toInt();
     size_t nk, nf, nb;
-    check(fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
+    check(api.fp8_block_mlp_bytes(M, K, F, flags, &nk, &nf, &nb), "fp8_block_mlp_bytes");
     const Tensor scratch = space(nb, dy.t);
     Tensor dX, dWgu, dWd;
     if (flags & FP8_BLOCK_NEED_DX) dX = make(grads[0].sizes(), dy.t);
     if (flags & FP8_BLOCK_NEED_DW) dWgu = make({K, 2 * F}, dy.t);
     if (flags & FP8_BLOCK_NEED_DW2) dWd = make({F, K}, dy.t);
-    check(fp8_block_mlp_bwd(dy.p(), dy.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dWgu), ptr(dWd),
+    check(api.fp8_block_mlp_bwd(dy.p(), dy.ld, M, K, F, flags, ptr(kept), nk, ptr(scratch), nb, ptr(dX), ptr(dWgu), ptr(dWd),
                             stream_of(dy.t)),
           "fp8_block_mlp_bwd");
     return once({dX, dWgu, dWd});
@@ -191,7 +214,7 @@ std::pair<Maybe, Maybe> quantize(const Tensor& x, int64_t fmt, bool rowwise, boo
   std::optional<Stored> q, t;
   if (rowwise) q.emplace(rows, cols, x);
   if (transposed) t.emplace(cols, rows, x);
-  check(fp8_block_quantize(x.data_ptr(), rows, cols, x.stride(0), (fp8_fmt)fmt, q ? q->codes : nullptr,
+  check(api.fp8_block_quantize(x.data_ptr(), rows, cols, x.stride(0), (fp8_fmt)fmt, q ? q->codes : nullptr,
                            q ? q->scales : nullptr, t ? t->codes : nullptr, t ? t->scales : nullptr, stream_of(x)),
         "fp8_block_quantize");
   return {q ? Maybe(q->data) : Maybe(), t ? Maybe(t->data) : Maybe()};
@@ -200,7 +223,7 @@ std::pair<Maybe, Maybe> quantize(const Tensor& x, int64_t fmt, bool rowwise, boo
 Tensor dequantize(const Tensor& data, int64_t rows, int64_t cols, int64_t fmt, const Maybe& out) {
   const Stored q(data, rows, cols);
   const Tensor o = out ? *out : make({rows, cols}, data);
-  check(fp8_block_dequantize(q.codes, q.scales, rows, cols, (fp8_fmt)fmt, o.data_ptr(), o.stride(0), stream_of(o)),
+  check(api.fp8_block_dequantize(q.codes, q.scales, rows, cols, (fp8_fmt)fmt, o.data_ptr(), o.stride(0), stream_of(o)),
         "fp8_block_dequantize");
   return o;
 }
@@ -210,14 +233,14 @@ Tensor serve(const Tensor& X, const Tensor& weight, int64_t N, const Maybe& out)
   const int64_t M = X.size(0), K = X.size(1);
   const Stored w(weight, N, K);
   const Tensor Y = out ? *out : make({M, N}, X);
-  if (fp8_block_linear_few(M, K, N)) {
-    check(fp8_block_linear_fwd_few(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, Y.data_ptr(), stream_of(X)),
+  if (api.fp8_block_linear_few(M, K, N)) {
+    check(api.fp8_block_linear_fwd_few(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, Y.data_ptr(), stream_of(X)),
           "fp8_block_linear_fwd_few");
     return Y;
   }
-  const size_t n = fp8_block_linear_cached_bytes(M, K, N);
+  const size_t n = api.fp8_block_linear_cached_bytes(M, K, N);
   const Tensor scratch = space(n, X);
-  check(fp8_block_linear_fwd_cached(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, ptr(scratch), n, Y.data_ptr(),
+  check(api.fp8_block_linear_fwd_cached(X.data_ptr(), X.stride(0), M, K, N, w.codes, w.scales, ptr(scratch), n, Y.data_ptr(),
                                     stream_of(X)),
         "fp8_block_linear_fwd_cached");
   return Y;
@@ -226,6 +249,7 @@ Tensor serve(const Tensor& X, const Tensor& weight, int64_t N, const Maybe& out)
 }  // namespace
 
 PYBIND11_MODULE(_block_binding, m) {
+  api.open((void*)py::module_::import("tensor_scaled_fp8_amd._lib").attr("load")().attr("_handle").cast<uintptr_t>());
   m.def("quantize", &quantize);
   m.def("dequantize", &dequantize);
   m.def("serve", &serve);
