@@ -616,6 +616,10 @@ fp8_status fp8_block_dequantize(const uint8_t* codes, const uint8_t* scales, int
  * split, the same result up to the order of the FP32 sums.
  */
 size_t fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t R);
+/* The tile of C that a workgroup of this product computes, and over how many
+ * workgroups the reduction of its last tiles is split (with that workspace;
+ * 1: none). For profiles and tests; any pointer may be NULL. */
+fp8_status fp8_block_gemm_plan(int64_t M, int64_t N, int64_t R, int* tile_m, int* tile_n, int* splits);
 fp8_status fp8_block_gemm(const uint8_t* A, const uint8_t* sA, fp8_fmt fa, const uint8_t* B, const uint8_t* sB,
                           fp8_fmt fb, int64_t M, int64_t N, int64_t R, void* C_bf16, int64_t ldc, void* ws,
                           size_t ws_bytes, hipStream_t stream);

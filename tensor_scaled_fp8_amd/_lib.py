@@ -14,6 +14,7 @@ c_int = ctypes.c_int
 c_vp = ctypes.c_void_p
 c_sz = ctypes.c_size_t
 c_szp = ctypes.POINTER(ctypes.c_size_t)
+c_intp = ctypes.POINTER(ctypes.c_int)
 
 # name -> (restype, argtypes); mirrors include/fp8lin.h
 SIGNATURES = {
@@ -55,6 +56,7 @@ SIGNATURES = {
     "fp8_block_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "fp8_block_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
     "fp8_block_gemm_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "fp8_block_gemm_plan": (c_int, [c_i64, c_i64, c_i64, c_intp, c_intp, c_intp]),
     "fp8_block_gemm": (c_int, [c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_sz,
                                c_vp]),
     "fp8_block_linear_bytes": (c_int, [c_i64, c_i64, c_i64, c_int, c_szp, c_szp, c_szp]),

@@ -63,6 +63,7 @@ struct BlockGemm {
   int64_t ldc;
 };
 size_t block_gemm_ws_bytes(int64_t M, int64_t N, int64_t R);
+void block_gemm_plan(int64_t M, int64_t N, int64_t R, int* tile_m, int* tile_n, int* splits);
 hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipStream_t st);
 
 // Y [M, N] bf16 (dense) = X [M, K] W for few rows of X, W stored as w [N, K]

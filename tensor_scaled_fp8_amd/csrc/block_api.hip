@@ -228,6 +228,17 @@ size_t fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t R) {
   return M < 0 || N < 0 || R < 0 ? 0 : block_gemm_ws_bytes(M, N, R);
 }
 
+fp8_status fp8_block_gemm_plan(int64_t M, int64_t N, int64_t R, int* tile_m, int* tile_n, int* splits) {
+  if (M < 0 || N < 0 || R < 0) return FP8_ERR_INVALID;
+  if (!size_ok(M, R) || !size_ok(N, R) || !size_ok(M, N)) return FP8_ERR_UNSUPPORTED;
+  int bm, bn, s;
+  block_gemm_plan(M, N, R, &bm, &bn, &s);
+  if (tile_m) *tile_m = bm;
+  if (tile_n) *tile_n = bn;
+  if (splits) *splits = s;
+  return FP8_OK;
+}
+
 fp8_status fp8_block_gemm(const uint8_t* A, const uint8_t* sA, fp8_fmt fa, const uint8_t* B, const uint8_t* sB,
                           fp8_fmt fb, int64_t M, int64_t N, int64_t R, void* C, int64_t ldc, void* ws, size_t ws_bytes,
                           hipStream_t stream) {

@@ -705,6 +705,13 @@ size_t block_gemm_ws_bytes(int64_t M, int64_t N, int64_t R) {
   return (size_t)(tiles % 256) * q.splits * q.bm * q.bn * 4;
 }
 
+void block_gemm_plan(int64_t M, int64_t N, int64_t R, int* tile_m, int* tile_n, int* splits) {
+  const Plan q = plan(M, N, round_blk(R) / kBlk, true);
+  *tile_m = q.bm;
+  *tile_n = q.bn;
+  *splits = q.splits;
+}
+
 hipError_t launch_block_gemm(const BlockGemm& g, void* ws, size_t ws_bytes, hipStream_t st) {
   const int64_t M = g.A.rows, N = g.B.rows, nk = round_blk(g.A.cols) / kBlk;
   if (M == 0 || N == 0) return hipSuccess;
