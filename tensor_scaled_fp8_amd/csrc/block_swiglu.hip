@@ -6,8 +6,8 @@
 // Everything is computed in 32 bits and rounded once, to bf16 or to a
 // block-scaled code. Bound by HBM: every input read once, every output
 // written once, the maxima of a block taken in registers. 4096 x 28672:
-// forward and backward 147 us each, 6.4 TB/s; the gradients of 2048 x 10240
-// straight to their stored forms 57 us, 3.3 TB/s (two waves a SIMD).
+// forward 147 us and backward 145, 6.4 TB/s; the gradients of 2048 x 10240
+// straight to their stored forms 56 us, 3.4 TB/s (two waves a SIMD).
 #include <type_traits>
 
 #include "block_quant.h"
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(Bf16Mat dh, BlockMat gq
 
 // One 128 x 128 tile: the E5M2 row and transposed forms of dg and du and
 // the E4M3 transposed form of h', all from one evaluation: a thread of 512
-// holds the three at 4 rows x 8 columns in 32 bits (96 of 172 registers, two
+// holds the three at 4 rows x 8 columns in 32 bits (96 of 144 registers, two
 // waves a SIMD; held to 128 registers it spilled, 57 -> 108 us) until the
 // columns' maxima are known. dh.p null: h' only.
 __device__ inline uint32_t bits_max(uint32_t a, uint32_t b) {
