@@ -43,15 +43,13 @@ def _check_bf16(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(pointer, row pitch) of a 2-D bf16 device matrix with contiguous rows."""
+def _check_rows(t: torch.Tensor, name: str) -> None:
+    """A 2-D bf16 device matrix with contiguous rows."""
     _check_bf16(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    ld, step = t.stride()
-    if step != 1 and t.shape[1] > 1:
+    if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), ld
 
 
 def _as_rows(t: torch.Tensor, name: str):
@@ -73,6 +71,7 @@ def _same_device(a: torch.Tensor, b: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be on {a.device}, got {b.device}")
 
 
+@functools.lru_cache(maxsize=4096)
 def _stored_bytes(rows: int, cols: int) -> int:
     pitch = _round(cols)
     return rows * pitch + _round(rows) * (pitch // BLOCK)
@@ -81,7 +80,7 @@ def _stored_bytes(rows: int, cols: int) -> int:
 def _check_data(data: torch.Tensor, rows: int, cols: int, name: str) -> None:
     if rows < 0 or cols < 0:
         raise ValueError(f"{name}: negative size [{rows}, {cols}]")
-    if data.dtype is not _U8 or data.dim() != 1 or not data.is_contiguous() or data.numel() != _stored_bytes(rows, cols):
+    if data.numel() != _stored_bytes(rows, cols) or data.dtype is not _U8 or data.dim() != 1 or not data.is_contiguous():
         raise ValueError(f"{name} must be {_stored_bytes(rows, cols)} contiguous bytes (uint8, 1-D) for "
                          f"[{rows}, {cols}], got {data.dtype} {tuple(data.shape)}")
 
@@ -157,7 +156,7 @@ def fp8_block_quantize(x: torch.Tensor, fmt="e4m3", rowwise: bool = True, transp
     """The stored form of a bf16 matrix x [rows, cols], blocks along its rows
     (rowwise), and of its transpose [cols, rows], blocks down the columns
     (transposed), from one read. Returns (BlockTensor or None, BlockTensor or None)."""
-    _rows(x, "x")
+    _check_rows(x, "x")
     rows, cols = x.shape
     f = _fmt(fmt)
     if not rowwise and not transposed:
@@ -174,7 +173,7 @@ def fp8_block_dequantize(q: BlockTensor, out: Optional[torch.Tensor] = None) -> 
     if out is not None:
         if tuple(out.shape) != (q.rows, q.cols):
             raise ValueError("out has the wrong shape")
-        _rows(out, "out")
+        _check_rows(out, "out")
         _same_device(q.data, out, "out")
     return _at(q.data, _binding().dequantize, q.data, q.rows, q.cols, q.fmt, out)
 
@@ -193,12 +192,12 @@ def fp8_block_gemm(a: BlockTensor, b: BlockTensor, out: Optional[torch.Tensor] =
         out = torch.empty((M, N), dtype=_BF16, device=a.device)
     if tuple(out.shape) != (M, N):
         raise ValueError("out has the wrong shape")
-    p, ld = _rows(out, "out")
+    _check_rows(out, "out")
     _same_device(a.data, out, "out")
     nb = _gemm_bytes(M, N, R)
     ws = torch.empty(nb, dtype=_U8, device=a.device) if nb else None
-    _launch(a.data, "fp8_block_gemm", *a.pointers(), a.fmt, *b.pointers(), b.fmt, M, N, R, p, ld,
-            ws.data_ptr() if nb else None, nb)
+    _launch(a.data, "fp8_block_gemm", *a.pointers(), a.fmt, *b.pointers(), b.fmt, M, N, R, out.data_ptr(),
+            out.stride(0), ws.data_ptr() if nb else None, nb)
     return out
 
 
@@ -278,7 +277,7 @@ def prepare_block_weight(W: torch.Tensor) -> BlockTensor:
 
 def fp8_block_linear_fwd_cached(X: torch.Tensor, w: BlockTensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [M, N] = X [M, K] W from a stored weight (prepare_block_weight)."""
-    _rows(X, "X")
+    _check_rows(X, "X")
     M, K = X.shape
     N = w.rows
     if w.cols != K or w.fmt != 0:
