@@ -684,9 +684,9 @@ fp8_status fp8_swiglu_bwd(const void* dh_bf16, int64_t lddh, int64_t rows, int64
  * value, the gradient of the gate and up values likewise (E5M2); the
  * backward recomputes h from the 8-bit gate and up. The first product and the
  * gradient of h are rounded to bf16 and then to 8 bits: what the products are
- * off (fp8_block_gemm) moves some values across a border of either, so dX and
- * dWgu are 0.0025 (rms, relative) off the same formulas in 64 bits, where FP32
- * products would give 0.0017, bf16's own rounding. Blocks along the 2 F
+ * off (fp8_block_gemm) moves some values across a border of either, so Y and
+ * dWd are 0.0021 and 0.0022 (rms, relative) off the same formulas in 64 bits,
+ * dX and dWgu 0.0025, where FP32 products give 0.0017, bf16's own rounding. Blocks along the 2 F
  * columns start anew at column F. Buffers as for the linear.
  */
 fp8_status fp8_block_mlp_bytes(int64_t M, int64_t K, int64_t F, int flags, size_t* kept, size_t* fwd_scratch,
