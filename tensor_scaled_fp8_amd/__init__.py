@@ -13,6 +13,8 @@ from .block import (BlockInferenceLinear, BlockLinear, BlockMLP, BlockTensor, bl
                     fp8_block_dequantize, fp8_block_gemm, fp8_block_linear_fwd_cached, fp8_block_quantize,
                     prepare_block_weight, swiglu)
 from .mu import MuScaler
+from .serving import (BlockKVCache, FP4InferenceLinear, FP4Tensor, InferenceAttention, fp4_linear_fwd_cached,
+                      fp8_cache_append, fp8_cache_attention, fp8_cache_read, prepare_fp4_weight)
 
 __all__ = [
     "FLAG_CLAMPED", "FLAG_NONFINITE", "FLAG_ZERO", "FP8_E4M3", "FP8_E5M2", "FP8_NOALLOC_SCRATCH_BYTES", "LIB_PATH", "SIGNATURES",
@@ -22,4 +24,6 @@ __all__ = [
     "prepare_weight", "read_scale", "release_workspaces",
     "BlockInferenceLinear", "BlockLinear", "BlockMLP", "BlockTensor", "block_linear", "block_mlp", "fp8_block_dequantize",
     "fp8_block_gemm", "fp8_block_linear_fwd_cached", "fp8_block_quantize", "prepare_block_weight", "swiglu",
+    "BlockKVCache", "FP4InferenceLinear", "FP4Tensor", "InferenceAttention", "fp4_linear_fwd_cached", "fp8_cache_append",
+    "fp8_cache_attention", "fp8_cache_read", "prepare_fp4_weight",
 ]

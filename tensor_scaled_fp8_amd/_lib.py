@@ -16,7 +16,7 @@ c_sz = ctypes.c_size_t
 c_szp = ctypes.POINTER(ctypes.c_size_t)
 c_intp = ctypes.POINTER(ctypes.c_int)
 
-# name -> (restype, argtypes); mirrors include/fp8lin.h
+# name -> (restype, argtypes); mirrors include/fp8lin.h and include/fp8lin_serve.h
 SIGNATURES = {
     "fp8_status_str": (ctypes.c_char_p, [c_int]),
     "fp8_abi_version": (c_int, []),
@@ -76,6 +76,20 @@ SIGNATURES = {
                                   c_sz, c_vp, c_vp]),
     "fp8_block_mlp_bwd": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_sz, c_vp, c_sz, c_vp, c_vp, c_vp,
                                   c_vp]),
+    # include/fp8lin_serve.h
+    "fp8_cache_codes_bytes": (c_sz, [c_i64, c_int, c_int, c_int]),
+    "fp8_cache_scales_bytes": (c_sz, [c_i64, c_int, c_int, c_int]),
+    "fp8_cache_append": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_vp, c_int, c_int, c_vp]),
+    "fp8_cache_read": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "fp8_cache_attention_workspace_bytes": (c_sz, [c_vp, c_vp, c_int]),
+    "fp8_cache_attention": (c_int, [c_vp, c_vp, c_vp, c_int, ctypes.c_float, ctypes.c_float, c_int, c_vp, c_vp, c_vp,
+                                    c_sz, c_vp]),
+    "fp4_codes_bytes": (c_sz, [c_i64, c_i64]),
+    "fp4_scales_bytes": (c_sz, [c_i64, c_i64]),
+    "fp4_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "fp4_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]),
+    "fp4_linear_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "fp4_linear_fwd_cached": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
 }
 
 FP8_E4M3, FP8_E5M2 = 0, 1

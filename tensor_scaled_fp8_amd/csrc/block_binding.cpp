@@ -12,6 +12,7 @@
 #include <optional>
 
 #include "fp8lin.h"
+#include "serve_binding.h"
 
 namespace {
 
@@ -249,11 +250,13 @@ Tensor serve(const Tensor& X, const Tensor& weight, int64_t N, const Maybe& out)
 }  // namespace
 
 PYBIND11_MODULE(_block_binding, m) {
-  api.open((void*)py::module_::import("tensor_scaled_fp8_amd._lib").attr("load")().attr("_handle").cast<uintptr_t>());
+  void* library = (void*)py::module_::import("tensor_scaled_fp8_amd._lib").attr("load")().attr("_handle").cast<uintptr_t>();
+  api.open(library);
   m.def("quantize", &quantize);
   m.def("dequantize", &dequantize);
   m.def("serve", &serve);
   m.def("linear", [](const Tensor& X, const Tensor& W) { return Linear::apply(X, W); });
   m.def("swiglu", [](const Tensor& gate, const Tensor& up) { return Swiglu::apply(gate, up); });
   m.def("mlp", [](const Tensor& X, const Tensor& Wgu, const Tensor& Wd) { return Mlp::apply(X, Wgu, Wd); });
+  bind_serve(m, library);
 }

@@ -1,0 +1,133 @@
+"""4-bit weights: stored and restored exactly, and the linear on them against
+the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import tensor_scaled_fp8_amd as tsf
+from tests.block_util import BF16_HALF, MFMA, held, to_bf16
+from tests.serve_util import GRID, fp4_held
+
+pytestmark = pytest.mark.gpu
+
+
+def up(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().to(torch.bfloat16)
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def weight(g, K, N):
+    return to_bf16(g.standard_normal((K, N)) * np.exp2(g.integers(-4, 4, size=(1, N))) * 0.02)
+
+
+@pytest.mark.parametrize("K,N", [(1, 1), (32, 16), (33, 17), (511, 40), (512, 3), (700, 65), (96, 300)])
+def test_store_and_restore(K, N):
+    g = np.random.Generator(np.random.PCG64(K + N))
+    w = weight(g, K, N)
+    wide = torch.zeros((K, N + 3), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:N + 1] = up(w)
+    q = tsf.prepare_fp4_weight(wide[:, 1:N + 1])
+    assert q.shape == (K, N) and q.nbytes == -(-N // 16) * -(-K // 512) * 4 * 1088
+    assert np.array_equal(host(q.dequantize()), fp4_held(w))
+
+
+def test_borders_and_extremes():
+    """Every value, the middles between them and their neighbours; subnormal, zero, infinite and NaN groups."""
+    mid = np.concatenate([GRID, (GRID[1:] + GRID[:-1]) / 2])
+    v = np.concatenate([mid, mid * (1 + 2.0 ** -7), mid * (1 - 2.0 ** -8), [0.1, 5.0, 6.0, 5.5]])
+    v = np.minimum(np.concatenate([v, -v]), 6)
+    w = np.zeros((32, 128))
+    for n in range(128):
+        w[0, n] = 6.0 * 2.0 ** (n % 40 - 20)
+        w[1:, n] = np.roll(v, 7 * n)[:31] * 2.0 ** (n % 40 - 20)
+    w[:, 100] = 0
+    w[:, 101] *= 2.0 ** -110
+    w[3, 102] = -np.inf
+    w[4, 103] = np.nan
+    w[:, 104] = np.sign(w[:, 104]) * 3.3e38
+    fin = np.isfinite(w)
+    w = np.where(fin, to_bf16(np.where(fin, w, 0)), w)
+    got, want = host(tsf.prepare_fp4_weight(up(w)).dequantize()), fp4_held(w)
+    # 3.3e38 is 3.88 of 2^126, held as 4: 2^128, to bf16 an infinity
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
+    bad = ~((got == want) | (np.isnan(got) & np.isnan(want)))
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+
+
+def check(x, w, y):
+    a, b = held(x), fp4_held(w)
+    want = a @ b
+    got = host(y)
+    assert got.shape == want.shape
+    bad = ~(np.abs(got - want) <= BF16_HALF * np.abs(want) + MFMA * (np.abs(a) @ np.abs(b)) + 2.0 ** -133)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:3], got[bad][:3], want[bad][:3])
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 128, 16), (1, 1, 1), (1, 7, 300), (2, 8, 5), (1, 1111, 777), (3, 2048, 130),
+                                   (4, 5000, 33), (16, 2048, 64), (7, 4700, 257), (13, 700, 1500), (1, 640, 9000),
+                                   (17, 130, 500), (31, 1100, 410), (33, 500, 420), (64, 512, 200), (65, 1000, 129),
+                                   (130, 1300, 300), (300, 260, 520), (257, 2100, 64)])
+def test_linear(M, K, N):
+    g = np.random.Generator(np.random.PCG64(M * K + N))
+    x = to_bf16(g.standard_normal((M, K)) * np.exp2(g.integers(-6, 6, size=(M, 1))))
+    w = weight(g, K, N)
+    q = tsf.prepare_fp4_weight(up(w))
+    y = tsf.fp4_linear_fwd_cached(up(x), q)
+    check(x, w, y)
+    wide = torch.full((M, K + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:K + 1] = up(x)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    assert tsf.fp4_linear_fwd_cached(wide[:, 1:K + 1], q, out) is out
+    assert torch.equal(out, y)                                             # any pitch, the same bits
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_linear_nonfinite(M):
+    """A NaN of X stays in its row, one of W in its column; an infinity of X saturates its block."""
+    g = np.random.Generator(np.random.PCG64(6))
+    K, N = 700, 210
+    x, w = to_bf16(g.standard_normal((M, K))), weight(g, K, N)
+    x[M - 1, 5] = np.inf
+    check(x, w, tsf.fp4_linear_fwd_cached(up(x), tsf.prepare_fp4_weight(up(w))))
+    x[0, 699], w[300, 77] = np.nan, np.nan
+    y = tsf.fp4_linear_fwd_cached(up(x), tsf.prepare_fp4_weight(up(w)))
+    nan = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    nan[0], nan[:, 77] = True, True
+    assert torch.equal(torch.isnan(y), nan)
+
+
+def test_empty():
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    w = tsf.prepare_fp4_weight(torch.ones((64, 48), **bf))
+    assert tsf.fp4_linear_fwd_cached(torch.ones((0, 64), **bf), w).shape == (0, 48)
+    w = tsf.prepare_fp4_weight(torch.ones((0, 48), **bf))
+    assert (tsf.fp4_linear_fwd_cached(torch.ones((3, 0), **bf), w) == 0).all()
+    w = tsf.prepare_fp4_weight(torch.ones((64, 0), **bf))
+    assert tsf.fp4_linear_fwd_cached(torch.ones((3, 64), **bf), w).shape == (3, 0)
+    assert w.dequantize().shape == (64, 0)
+
+
+def test_in_a_graph_and_module():
+    g = np.random.Generator(np.random.PCG64(7))
+    K, N = 900, 600
+    lin = tsf.FP4InferenceLinear(up(weight(g, K, N)))
+    x = up(g.standard_normal((2, 3, K)))
+    lin(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+    for _ in range(3):
+        new = up(g.standard_normal((2, 3, K)))
+        want = lin(new)
+        x.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert y.shape == (2, 3, N) and torch.equal(y, want)
+    state = lin.state_dict()
+    other = tsf.FP4InferenceLinear(torch.zeros((K, N), dtype=torch.bfloat16, device="cuda"))
+    other.load_state_dict(state)
+    assert torch.equal(other(x), want)
