@@ -1,9 +1,10 @@
 // Attention over the paged 8-bit cache.
 //
-// A workgroup takes R = 16 rows of one key head, a row being one of the
-// head's queries of one token, and the tokens they see; its waves share out
-// the tokens, 32 (two blocks) at a time, each with a softmax of its own
-// (running maximum, sum, weighted values), joined over LDS at the end.
+// A workgroup's tile is R = 16 MT rows of one key head, a row being one of
+// the head's queries of one token, and a range of the tokens that they see;
+// its waves share out the tokens, 32 (two blocks) at a time, each with a
+// softmax of its own (running maximum, sum, weighted values), joined over LDS
+// at the tile's end.
 //   s^T [tokens, rows] = K Q^T and o^T [D, rows] += V^T p^T by 16x16x32 bf16
 // products: K and V come as the first operand straight from memory (the
 // cache holds them in its order), converted to bf16 by the instruction that
@@ -14,6 +15,18 @@
 // The running maximum moves only when a score exceeds it by 2^8: until then
 // the weights are scaled by up to 2^8, which costs neither range nor
 // precision, and no lane has to know of another's scores.
+//
+// FINE: a weight goes into the product as two bf16, its rounding and what
+// that left (2^-17 of it): the outputs are then bf16's own rounding off and no
+// more. It costs a second product of V and a third of the softmax, which a
+// call that waits for the cache's bytes does not notice.
+//
+// Few rows (a decode batch): the work of all (sequence, tile, head) is one
+// line of units of 128 tokens, cut into equal shares, one a workgroup, as
+// many as the chip holds at once: whatever the lengths, all CUs end together.
+// A tile cut by a share's end leaves its parts' sums in the workspace, and a
+// second launch joins them. Many rows (prompts): one workgroup a tile, the
+// longest first.
 #include "cache.h"
 
 namespace fp8lin {
@@ -41,6 +54,8 @@ __device__ inline bq_f32x4 mma(ca_bf16x8 a, ca_bf16x8 b, bq_f32x4 c) {
 __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ inline float nan() { return __uint_as_float(0x7FC00000u); }
 
+__device__ inline uint32_t high_half(uint32_t w) { return w & 0xFFFF0000u; }
+
 // over the four lanes that share lane % 16
 __device__ inline float quad_max(float a) {
   a = fmaxf(a, __shfl_xor(a, 16));
@@ -63,98 +78,198 @@ __device__ inline uint32_t nan_bytes(uint32_t w) {
   const uint32_t m = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
   return m * 0xFFu;
 }
+__device__ inline float lse_of(float m, float sum) {
+  return sum == 0 ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
 
-template <int D>
-struct State {
-  float m, l;  // of this lane's row; l over this lane's tokens
-  bq_f32x4 o[D / 16];
-};
+constexpr int kGroup = 32;                // tokens of a wave's step
+constexpr int kStep = kGroup * kWaves;    // of a workgroup's
+constexpr int kStepLog = 7;
+static_assert(kStep == 1 << kStepLog, "a step's tokens");
+constexpr int kShares = 512;              // two workgroups a CU
+constexpr int64_t kMostTokens = ((int64_t)1 << 31) - 256;
 
-// One row's tile of a sequence
+// A value that all lanes have, to scalar registers
+__device__ inline int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline int64_t uni(int64_t x) {
+  return (int64_t)(uint32_t)uni((int)x) | (int64_t)uni((int)(x >> 32)) << 32;
+}
+__device__ inline Seq uni(Seq s) { return {uni(s.row0), uni(s.n), uni(s.p0)}; }
+
+// One tile of a sequence
 struct Tile {
   int seq, h;
   Seq s;
-  int r0;          // its first row of the sequence's n * group
-  int first, last; // positions of the first and the last row's token (last < first: no rows)
+  int r0;           // its first row of the sequence's n * group
+  int first, last;  // positions of the first and the last row's token
+};
+template <int R>
+__device__ inline bool tile_at(const CacheAttend& a, int seq, const Seq& s, int at, int h, Tile& t) {
+  t.seq = seq;
+  t.h = h;
+  t.s = s;
+  const int rows = s.n * a.group;
+  if (at < 0 || at > (rows - 1) / R || rows == 0) return false;
+  t.r0 = at * R;
+  const int end = rows - t.r0 > R ? t.r0 + R : rows;
+  t.first = uni((int)s.p0 + t.r0 / a.group);
+  t.last = uni((int)s.p0 + (end - 1) / a.group);
+  return true;
+}
+// The tokens that rows of positions first .. last see: from a multiple of 32
+struct Span {
+  int64_t from, to;
+};
+__device__ inline Span span_of(const CacheAttend& a, int64_t first, int64_t last) {
+  int64_t have = a.b.table_pages << a.c.shift;
+  if (have > kMostTokens) have = kMostTokens;
+  Span s;
+  s.to = last + 1 < have ? last + 1 : have;
+  s.from = a.window > 0 && first - a.window + 1 > 0 ? (first - a.window + 1) / kGroup * kGroup : 0;
+  if (s.to < s.from) s.to = s.from;
+  return s;
+}
+
+template <int D, int MT>
+struct State {
+  float m[MT], l[MT];  // of this lane's row of each 16; l over this lane's tokens
+  bq_f32x4 o[MT][D / 16];
+};
+// 32 tokens' codes, of the keys or of the values
+template <int D>
+struct Codes {
+  ca_u32x4 w[2][D / 64];
 };
 
-// 32 tokens from j0 into a wave's state. HARD: the mask hides some of them
-// from some rows; pos is the lane's row's position (-1: no row).
-template <int D, bool CAP>
-__device__ inline void attend_group(const CacheAttend& a, const Tile& t, int64_t j0, int hi, int pos,
-                                    const ca_bf16x8 (&qf)[D / 32], State<D>& st, int lane) {
-  constexpr int P = D / 64;
-  const int lo16 = lane & 15, g = lane >> 4;
-  ca_u32x4 kc[2][P], vc[2][P];
-  float ks[2], vs[2];
+// The blocks of a wave's next 32 steps: lane 2 n + b has block b of step n
+struct Blocks {
+  uint32_t lo, hi;  // its number; hi < 0: it is not there
+  uint32_t scales;  // bytes of K and V
+};
+__device__ inline Blocks blocks_of(const CacheAttend& a, const Tile& t, int64_t j, int64_t to, int lane) {
+  j += (lane >> 1) * kStep + 16 * (lane & 1);
+  const int64_t blk = j < to ? block_at(a.c, a.b, t.seq, j, t.h) : -1;
+  Blocks b = {(uint32_t)blk, (uint32_t)(blk >> 32), 127u | 127u << 8};
+  if (blk >= 0) b.scales = *(const uint16_t*)(a.c.scales + 2 * blk);
+  return b;
+}
+// Issues the loads of step n's codes. A block that is not there is read as
+// zeros, and so is every block if there is no such step: loads that depend on
+// no branch can be waited for singly.
+template <int D, bool V>
+__device__ inline void load_codes(const CacheAttend& a, const Blocks& bl, int n, bool real, int lane, Codes<D>& c) {
+  const int off = 16 * lane;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const uint32_t lo = __builtin_amdgcn_readlane(bl.lo, 2 * n + b), hi = __builtin_amdgcn_readlane(bl.hi, 2 * n + b);
+    const bool there = (int)hi >= 0 && real;
+    const int64_t blk = there ? (int64_t)((uint64_t)hi << 32 | lo) : 0;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((V ? a.c.v : a.c.k) + blk * (kTok * D), (short)0,
+                                                                       there ? kTok * D : 0, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) c.w[b][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off + 1024 * i, 0, 0);
+  }
+}
+// Step n's scales
+struct Scales {
+  float k[2], v[2];
   bool there[2];
+};
+__device__ inline Scales scales_of(const Blocks& bl, int n) {
+  Scales s;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const int64_t blk = j0 + 16 * b < hi ? block_at(a.c, a.b, t.seq, j0 + 16 * b, t.h) : -1;
-    there[b] = blk >= 0;
-    ks[b] = vs[b] = 1.0f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) kc[b][i] = vc[b][i] = (ca_u32x4){0, 0, 0, 0};
-    if (there[b]) {
-      const uint32_t sc = *(const uint16_t*)(a.c.scales + 2 * blk);
-      ks[b] = scale_value(sc & 0xFFu);
-      vs[b] = scale_value(sc >> 8);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        kc[b][i] = *(const ca_u32x4*)(a.c.k + blk * (kTok * D) + 1024 * i + 16 * lane);
-        vc[b][i] = *(const ca_u32x4*)(a.c.v + blk * (kTok * D) + 1024 * i + 16 * lane);
-      }
-    }
+    const uint32_t sc = __builtin_amdgcn_readlane(bl.scales, 2 * n + b);
+    s.k[b] = scale_value(sc & 0xFFu);
+    s.v[b] = scale_value(sc >> 8);
+    s.there[b] = (int)__builtin_amdgcn_readlane(bl.hi, 2 * n + b) >= 0;
   }
-  float s[8];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    bq_f32x4 c = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      c = mma(widen(kc[b][i].x, ks[b], kc[b][i].y, ks[b]), qf[2 * i], c);
-      c = mma(widen(kc[b][i].z, ks[b], kc[b][i].w, ks[b]), qf[2 * i + 1], c);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[4 * b + i] = c[i] * a.scale;
-      if constexpr (CAP) s[4 * b + i] = a.cap * tanh_(s[4 * b + i] / a.cap);
-      s[4 * b + i] *= kLog2e;
-    }
-  }
+  return s;
+}
+
+// Queries as the second operand: of few rows in registers, else in LDS
+template <int D, int MT>
+struct Queries {
+  ca_bf16x8 f[D / 32];
+  __device__ ca_bf16x8 get(int, int i) const { return f[i]; }
+};
+
+// 32 tokens from j0 into a wave's state; pos: the positions of the lane's rows
+// (-1: no row). next_k, next_v issue the next step's loads, as soon as this
+// one's codes are used.
+template <int D, int MT, bool CAP, bool FINE, typename Q, typename NextK, typename NextV>
+__device__ inline void attend_group(const CacheAttend& a, const Tile& t, int j0, const int (&pos)[MT], const Q& query,
+                                    int g, const Scales& sc, Codes<D>& k, Codes<D>& c, State<D, MT>& st, NextK next_k,
+                                    NextV next_v) {
+  constexpr int P = D / 64;
   // hidden from somebody: the rows' positions are first .. last
-  const bool hard = !there[0] || !there[1] || j0 + 31 > t.first || (a.window > 0 && j0 <= (int64_t)t.last - a.window);
-  bool seen[8];
+  const bool hard = !sc.there[0] | !sc.there[1] | (j0 + 31 > t.first) | ((a.window > 0) & (j0 <= t.last - a.window));
+  const float unit = CAP ? a.scale : a.scale * kLog2e;
+  const auto key = [&](int b, int i) {
+    const ca_u32x4 w = k.w[b][i / 2];
+    return i & 1 ? widen(w.z, sc.k[b], w.w, sc.k[b]) : widen(w.x, sc.k[b], w.y, sc.k[b]);
+  };
+  ca_bf16x8 kf[2][MT > 1 ? 2 * P : 1];  // one row tile takes them as they are widened
+  if constexpr (MT > 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) seen[i] = true;
-  if (hard) {
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 2 * P; ++i) kf[b][i] = key(b, i);
+    next_k();
+  }
+  uint32_t seen[MT];  // bit i: the row sees token i of the lane's 8
+  ca_bf16x8 pf[MT], pl[FINE ? MT : 1];
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    float s[8];
+    bq_f32x4 x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i) {
+      const ca_bf16x8 q = query.get(r, i);
+      x0 = mma(MT > 1 ? kf[0][MT > 1 ? i : 0] : key(0, i), q, x0);
+      x1 = mma(MT > 1 ? kf[1][MT > 1 ? i : 0] : key(1, i), q, x1);
+    }
+    if constexpr (MT == 1) next_k();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-      seen[i] = there[i >> 2] && j <= pos && (a.window <= 0 || j > (int64_t)pos - a.window);
-      if (!seen[i]) s[i] = -__builtin_inff();
+      s[i] = (i < 4 ? x0[i & 3] : x1[i & 3]) * unit;
+      if constexpr (CAP) s[i] = a.cap * kLog2e * tanh_(s[i] / a.cap);
     }
-  }
-  float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-  if (__any(top > st.m + kSlack)) {
-    const float m = fmaxf(quad_max(top), st.m);
-    const float f = m == st.m ? 1.0f : exp2_(st.m - m);
-    st.m = m;
-    st.l *= f;
+    if (hard) {
+      seen[r] = 0;
+      const int low = a.window > 0 ? pos[r] - a.window : -1;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.o[i] *= f;
-  }
-  const float base = st.m == -__builtin_inff() ? 0.0f : st.m;
-  ca_u32x4 pw;
-  float p[8];
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+        const bool is = sc.there[i >> 2] & (j <= pos[r]) & (j > low);
+        seen[r] |= is ? 1u << i : 0u;
+        if (!is) s[i] = -__builtin_inff();
+      }
+    }
+    const float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+    if (__any(top > st.m[r] + kSlack)) {
+      const float m = fmaxf(quad_max(top), st.m[r]);
+      const float f = m == st.m[r] ? 1.0f : exp2_(st.m[r] - m);
+      st.m[r] = m;
+      st.l[r] *= f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p[i] = exp2_(s[i] - base);
-    st.l += p[i];
-  }
+      for (int i = 0; i < D / 16; ++i) st.o[r][i] *= f;
+    }
+    const float base = st.m[r] == -__builtin_inff() ? 0.0f : st.m[r];
+    float p[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pw[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-  const ca_bf16x8 pf = __builtin_bit_cast(ca_bf16x8, pw);
+    for (int i = 0; i < 8; ++i) p[i] = exp2_(s[i] - base);
+    st.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    ca_u32x4 w, x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+      if constexpr (FINE)
+        x[i] = pack_bf16(p[2 * i] - __uint_as_float(w[i] << 16), p[2 * i + 1] - __uint_as_float(high_half(w[i])));
+    }
+    pf[r] = __builtin_bit_cast(ca_bf16x8, w);
+    if constexpr (FINE) pl[r] = __builtin_bit_cast(ca_bf16x8, x);
+  }
   if (hard) {
     // a hidden token's weight is 0, but a NaN times 0 is one: the NaNs are
     // taken out of the product, and given to the rows that see them
@@ -164,151 +279,443 @@ __device__ inline void attend_group(const CacheAttend& a, const Tile& t, int64_t
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) any |= nan_bytes(vc[b][i][k]);
+        for (int k = 0; k < 4; ++k) any |= nan_bytes(c.w[b][i][k]);
     if (__any(any != 0)) {
-      ca_u32x4 sw;
+      // found anew: 32 registers less than held from the search
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sw[i] = (seen[2 * i] ? 0x3F80u : 0u) | (seen[2 * i + 1] ? 0x3F800000u : 0u);
-      const ca_bf16x8 sf = __builtin_bit_cast(ca_bf16x8, sw);
+      for (int i = 0; i < P; ++i) asm volatile("" : "+v"(c.w[0][i]), "+v"(c.w[1][i]));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t n[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          n[b] = nan_bytes(vc[b][i / 4][i % 4]);
-          vc[b][i / 4][i % 4] &= ~n[b];
+          n[b] = nan_bytes(c.w[b][i / 4][i % 4]);
+          c.w[b][i / 4][i % 4] &= ~n[b];
           n[b] &= 0x38383838u;  // 1
         }
-        const bq_f32x4 c = mma(widen(n[0], 1.0f, n[1], 1.0f), sf, (bq_f32x4){0, 0, 0, 0});
+        const ca_bf16x8 nf = widen(n[0], 1.0f, n[1], 1.0f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (c[k] > 0) st.o[i][k] = nan();
+        for (int r = 0; r < MT; ++r) {
+          ca_u32x4 w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = (seen[r] >> (2 * k) & 1u) * 0x3F80u | (seen[r] >> (2 * k + 1) & 1u) * 0x3F800000u;
+          const bq_f32x4 x = mma(nf, __builtin_bit_cast(ca_bf16x8, w), (bq_f32x4){0, 0, 0, 0});
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (x[k] > 0) st.o[r][i][k] = nan();
+        }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-    st.o[i] = mma(widen(vc[0][i / 4][i % 4], vs[0], vc[1][i / 4][i % 4], vs[1]), pf, st.o[i]);
+  for (int i = 0; i < D / 16; ++i) {
+    const ca_bf16x8 vf = widen(c.w[0][i / 4][i % 4], sc.v[0], c.w[1][i / 4][i % 4], sc.v[1]);
+#pragma unroll
+    for (int r = 0; r < MT; ++r) {
+      st.o[r][i] = mma(vf, pf[r], st.o[r][i]);
+      if constexpr (FINE) st.o[r][i] = mma(vf, pl[r], st.o[r][i]);
+    }
+  }
+  next_v();
 }
 
-// The tile that virtual tile v is: sequence i's tiles of R rows start at
-// starts[i] group / R + i
-template <int R>
-__device__ inline bool tile_of(const CacheAttend& a, int64_t v, int h, Tile& t) {
-  int64_t at;
-  if (a.b.starts) {
-    const auto first = [&](int j) { return (int64_t)start_of(a.b, j) * a.group / R + j; };
-    t.seq = last_upto(a.b.sequences, v, first);
-    at = v - first(t.seq);
-  } else {
-    const int per = (a.group + R - 1) / R;
-    t.seq = (int)(v / per);
-    at = v - (int64_t)t.seq * per;
-  }
-  t.h = h;
-  t.s = seq_of(a.b, t.seq);
-  const int64_t rows = (int64_t)t.s.n * a.group;
-  if (at < 0 || at * R >= rows) return false;
-  t.r0 = (int)(at * R);
-  const int64_t end = at * R + R < rows ? at * R + R : rows;
-  t.first = (int)(t.s.p0 + t.r0 / a.group);
-  t.last = (int)(t.s.p0 + (end - 1) / a.group);
-  return true;
-}
+// Where a tile's part goes: parts[slot][row][D] and the row's maximum and sum
+struct Space {
+  float* parts;
+  float* sums;  // [slot][row][2]
+  int4* heads;  // [share]: parts of the tile that starts in it and ends in a later one, sequence, head, first row
+};
 
-template <int D, bool CAP>
-__global__ __launch_bounds__(64 * kWaves) void cache_attention_kernel(CacheAttend a) {
-  constexpr int R = 16, W = D / 16;
-  constexpr int C = W < 8 ? W : 8;  // joined at a time
-  __shared__ float acc[kWaves][4][C][64];
-  __shared__ float ml[kWaves][2][R];
-  Tile t;
-  if (!tile_of<R>(a, blockIdx.x / a.c.heads, blockIdx.x % a.c.heads, t)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lo16 = lane & 15, g = lane >> 4;
-  const int64_t row = t.r0 + lo16;
-  const bool mine = row < (int64_t)t.s.n * a.group;
-  const int tok = (int)(row / a.group), head = t.h * a.group + (int)(row % a.group);
-  const int pos = mine ? (int)(t.s.p0 + tok) : -1;
-  const int64_t have = a.b.table_pages << a.c.shift;
-  const int hi = (int)(t.last + 1 < have ? t.last + 1 : have);
-  const int64_t from = a.window > 0 && (int64_t)t.first - a.window + 1 > 0 ? (int64_t)t.first - a.window + 1 : 0;
-  ca_bf16x8 qf[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    ca_u32x4 w = {0, 0, 0, 0};
-    if (mine)
-      w = *(const bq_u32x4_a2*)(a.q.p + (int64_t)(t.s.row0 + tok) * a.q.tok + head * a.q.head + 64 * (i / 2) + 16 * g +
-                                8 * (i % 2));
-    qf[i] = __builtin_bit_cast(ca_bf16x8, w);
-  }
-  State<D> st;
-  st.m = -__builtin_inff();
-  st.l = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) st.o[i] = (bq_f32x4){0, 0, 0, 0};
-  for (int64_t j0 = (from / 32 + wave) * 32; j0 < hi; j0 += 32 * kWaves)
-    attend_group<D, CAP>(a, t, j0, hi, pos, qf, st, lane);
-  const float l = quad_sum(st.l);
-  if (lane < R) {
-    ml[wave][0][lane] = st.m;
-    ml[wave][1][lane] = l;
-  }
-  __syncthreads();
-  float m = ml[0][0][lo16], sum = 0, f[kWaves];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, ml[w][0][lo16]);
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const float mw = ml[w][0][lo16];
-    f[w] = mw == m ? 1.0f : exp2_(mw - m);
-    sum += ml[w][1][lo16] * f[w];
-  }
-  const int64_t tr = t.s.row0 + tok;
-  const float inv = sum == 0 ? 0.0f : 1.0f / sum;
-  uint16_t* out = a.out.p + tr * a.out.tok + head * a.out.head + W * (4 * g + wave);
-#pragma unroll
-  for (int c = 0; c < W; c += C) {
-    if (c) __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < C; ++i) acc[wave][k][i][lane] = st.o[c + i][k];
-    __syncthreads();
-    float o[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += acc[w][wave][i][lane] * f[w];
-    if (mine)
-#pragma unroll
-      for (int i = 0; i < C; i += 4)
-        *(bq_u32x2_a2*)(out + c + i) =
-            (bq_u32x2){pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv)};
-  }
-  if (mine && a.lse && wave == 0 && g == 0)
-    a.lse[tr * a.q_heads + head] = sum == 0 ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-}
+template <int D, int MT>
+struct Shared {
+  float acc[kWaves][4][D / 16 < 8 ? D / 16 : 8][64];
+  float ml[kWaves][2][16 * MT];
+  ca_u32x4 q[MT > 1 ? MT : 1][MT > 1 ? D / 32 : 1][MT > 1 ? 64 : 1];
+};
+template <int D, int MT>
+struct LdsQueries {
+  const Shared<D, MT>& s;
+  int lane;
+  __device__ ca_bf16x8 get(int r, int i) const { return __builtin_bit_cast(ca_bf16x8, s.q[r][i][lane]); }
+};
 
 template <int D>
-hipError_t run(const CacheAttend& a, hipStream_t st) {
-  const int64_t tiles = a.b.starts ? (int64_t)a.b.tokens * a.group / 16 + a.b.sequences
-                                   : (int64_t)a.b.sequences * ((a.group + 15) / 16);
-  const unsigned grid = (unsigned)(tiles * a.c.heads);
-  if (a.cap > 0) cache_attention_kernel<D, true><<<grid, 64 * kWaves, 0, st>>>(a);
-  else cache_attention_kernel<D, false><<<grid, 64 * kWaves, 0, st>>>(a);
+__device__ inline ca_u32x4 query_at(const CacheAttend& a, const Tile& t, int row, int i, int g) {
+  if (row >= t.s.n * a.group) return (ca_u32x4){0, 0, 0, 0};
+  const int tok = row / a.group, head = t.h * a.group + row % a.group;
+  return *(const bq_u32x4_a2*)(a.q.p + (int64_t)(t.s.row0 + tok) * a.q.tok + head * a.q.head + 64 * (i / 2) + 16 * g +
+                               8 * (i % 2));
+}
+
+// The waves' sums (their maxima and sums are in sh.ml already) joined and written
+template <int D, int MT>
+__device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& ws, int slot, Shared<D, MT>& sh,
+                              const State<D, MT>& st, int lane, int wave) {
+  constexpr int R = 16 * MT, W = D / 16, C = W < 8 ? W : 8;
+  const int lo16 = lane & 15, g = lane >> 4, rows = t.s.n * a.group;
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    const int row = 16 * r + lo16;
+    float m = sh.ml[0][0][row], sum = 0, f[kWaves];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.ml[w][0][row]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = sh.ml[w][0][row];
+      f[w] = mw == m ? 1.0f : exp2_(mw - m);
+      sum += sh.ml[w][1][row] * f[w];
+    }
+    const bool have = t.r0 + row < rows;
+    const int tok = (t.r0 + row) / a.group, head = t.h * a.group + (t.r0 + row) % a.group;
+    const int64_t tr = t.s.row0 + tok;
+    const float inv = sum == 0 ? 0.0f : 1.0f / sum;
+    const int d = W * (4 * g + wave);  // this lane's D / 16 elements
+    uint16_t* out = a.out.p + tr * a.out.tok + head * a.out.head + d;
+    float* part = ws.parts + ((int64_t)slot * R + row) * D + d;
+#pragma unroll
+    for (int c = 0; c < W; c += C) {
+      if (r || c) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < C; ++i) sh.acc[wave][k][i][lane] = st.o[r][c + i][k];
+      __syncthreads();
+      float o[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] += sh.acc[w][wave][i][lane] * f[w];
+      if (!have) continue;
+      if (slot >= 0) {
+#pragma unroll
+        for (int i = 0; i < C; i += 4) *(bq_f32x4*)(part + c + i) = (bq_f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; i += 4)
+          *(bq_u32x2_a2*)(out + c + i) =
+              (bq_u32x2){pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv)};
+      }
+    }
+    if (have && wave == 0 && g == 0) {
+      if (slot >= 0) {
+        ws.sums[((int64_t)slot * R + row) * 2] = m;
+        ws.sums[((int64_t)slot * R + row) * 2 + 1] = sum;
+      } else if (a.lse) {
+        a.lse[tr * a.q_heads + head] = lse_of(m, sum);
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The tile's tokens from .. to (from a multiple of 32): its output, or with
+// slot >= 0 a part of it.
+template <int D, int MT, bool CAP, bool FINE>
+__device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t from, int64_t to, const Space& ws, int slot,
+                                Shared<D, MT>& sh) {
+  constexpr int R = 16 * MT, W = D / 16, C = W < 8 ? W : 8;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // nothing is held from tile to tile
+  const int wave = uni((int)(threadIdx.x >> 6));
+  const int lo16 = lane & 15, g = lane >> 4;
+  const int rows = t.s.n * a.group;
+  from = uni(from);
+  to = uni(to);
+  const int64_t j = from + wave * kGroup;
+  const int steps = j < to ? (int)((to - j + kStep - 1) / kStep) : 0;
+  Blocks bl = blocks_of(a, t, j, to, lane);
+  int pos[MT];
+  State<D, MT> st;
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    const int row = t.r0 + 16 * r + lo16;
+    pos[r] = row < rows ? (int)t.s.p0 + row / a.group : -1;
+    st.m[r] = -__builtin_inff();
+    st.l[r] = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) st.o[r][i] = (bq_f32x4){0, 0, 0, 0};
+  }
+  Queries<D, MT> mine;
+  if constexpr (MT == 1) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) mine.f[i] = __builtin_bit_cast(ca_bf16x8, query_at<D>(a, t, t.r0 + lo16, i, g));
+  } else {
+    for (int n = wave; n < MT * (D / 32); n += kWaves)
+      sh.q[n / (D / 32)][n % (D / 32)][lane] = query_at<D>(a, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
+    __syncthreads();
+  }
+  Codes<D> k, v;
+  load_codes<D, false>(a, bl, 0, steps > 0, lane, k);
+  load_codes<D, true>(a, bl, 0, steps > 0, lane, v);
+  for (int n = 0; n < steps; ++n) {
+    const int j0 = (int)(j + (int64_t)n * kStep), next = (n + 1) & 31;
+    const bool more = n + 1 < steps;
+    const auto next_k = [&] { load_codes<D, false>(a, bl, next, more, lane, k); };
+    const auto next_v = [&] { load_codes<D, true>(a, bl, next, more, lane, v); };
+    const Scales sc = scales_of(bl, n & 31);
+    if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * kStep, to, lane);
+    if constexpr (MT == 1) attend_group<D, MT, CAP, FINE>(a, t, j0, pos, mine, g, sc, k, v, st, next_k, next_v);
+    else attend_group<D, MT, CAP, FINE>(a, t, j0, pos, LdsQueries<D, MT>{sh, lane}, g, sc, k, v, st, next_k, next_v);
+  }
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    const float l = quad_sum(st.l[r]);
+    if (lane < 16) {
+      sh.ml[wave][0][16 * r + lane] = st.m[r];
+      sh.ml[wave][1][16 * r + lane] = l;
+    }
+  }
+  __syncthreads();
+  // what follows is computed here, and not held in registers through the loop
+  int lane_ = lane;
+  asm volatile("" : "+v"(lane_));
+  finish<D, MT>(a, t, ws, slot, sh, st, lane_, wave);
+}
+
+// A share is counted in units of 128 2^shift tokens (so that all of a call's
+// are fewer than 2^31). A tile costs those that its sequence's rows see, and
+// kBegin more: its lookups and first loads, which nothing overlaps, and its
+// join over LDS take as long as two units (a layer's decode step of 32
+// sequences of 50 to 8192 tokens, 32 heads: 203 us counted as 0, 149 as 1, 141
+// as 2, 144 as 4).
+constexpr int kBegin = 2;
+struct Units {
+  int tiles, units;
+  int64_t from;  // the first one's first token
+};
+template <int R>
+__device__ inline Units units_of(const CacheAttend& a, const Seq& s, int shift) {
+  const Span p = span_of(a, s.p0, s.p0 + s.n - 1);
+  return {(s.n * a.group + R - 1) / R, (int)((p.to - p.from + (kStep << shift) - 1) >> (kStepLog + shift)) + kBegin, p.from};
+}
+
+// sum over the lanes up to this one
+__device__ inline int scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
+template <int D, int MT, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_shares_kernel(CacheAttend a, Space ws, int shift) {
+  constexpr int R = 16 * MT;
+  __shared__ Shared<D, MT> sh;
+  const int lane = threadIdx.x & 63;
+  // units before each lane's sequences; every wave finds its workgroup's place by itself
+  const int per = (a.b.sequences + 63) / 64;
+  int mine = 0;
+  Seq s = {0, 0, 0};
+  for (int i = lane * per; i < (lane + 1) * per && i < a.b.sequences; ++i) {
+    s = seq_of(a.b, i);
+    const Units n = units_of<R>(a, s, shift);
+    mine += n.tiles * a.c.heads * n.units;
+  }
+  const int upto = scan(mine), total = __builtin_amdgcn_readlane(upto, 63);
+  const int share = (int)(((int64_t)total + kShares - 1) / kShares);
+  int u = blockIdx.x * share;
+  const int end = total - u < share ? total : u + share;
+  int4 open = {0, 0, 0, 0};
+  if (share > 0 && u < end) {
+    const int at_lane = 63 - __builtin_clzll(__ballot(upto - mine <= u));
+    int rem = u - __builtin_amdgcn_readlane(upto - mine, at_lane), seq = at_lane * per;
+    s = {__builtin_amdgcn_readlane(s.row0, at_lane), __builtin_amdgcn_readlane(s.n, at_lane),
+         (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)s.p0, at_lane) |
+             (int64_t)__builtin_amdgcn_readlane((int)(s.p0 >> 32), at_lane) << 32};
+    bool known = per == 1, found = false;  // s is seq's; and the place in its tiles
+    Units n = {0, 0, 0};
+    int k0 = 0, at = 0, h = 0;
+    while (u < end) {
+      if (!found) {
+        if (!known) s = uni(seq_of(a.b, seq));
+        known = false;
+        n = units_of<R>(a, s, shift);
+        n = {uni(n.tiles), uni(n.units), uni(n.from)};
+        if (rem >= n.tiles * a.c.heads * n.units) {
+          rem -= n.tiles * a.c.heads * n.units;
+          ++seq;
+          continue;
+        }
+        const int item = uni((int)((uint32_t)rem / (uint32_t)n.units));
+        k0 = rem - item * n.units;
+        h = uni((int)((uint32_t)item / (uint32_t)n.tiles));
+        at = item - h * n.tiles;
+        found = true;
+      }
+      const int k1 = end - u < n.units - k0 ? k0 + (end - u) : n.units;
+      if (k1 > kBegin) {
+        Tile t;
+        tile_at<R>(a, seq, s, at, h, t);
+        const Span own = span_of(a, t.first, t.last);
+        const bool first = k0 <= kBegin, whole = first && k1 == n.units;
+        const int64_t lo = n.from + ((int64_t)(first ? 0 : k0 - kBegin) * kStep << shift);
+        const int64_t hi = n.from + ((int64_t)(k1 - kBegin) * kStep << shift);
+        const int64_t from = lo > own.from ? lo : own.from, to = hi < own.to ? hi : own.to;
+        run_tile<D, MT, CAP, true>(a, t, from, to, ws, whole ? -1 : 2 * (int)blockIdx.x + first, sh);
+        if (first && !whole)
+          open = make_int4(1 + (u + (n.units - k0) - 1) / share - (int)blockIdx.x, seq, t.h, t.r0);
+      } else if (n.units == kBegin) {
+        // it sees nothing
+        Tile t;
+        tile_at<R>(a, seq, s, at, h, t);
+        if (k1 == n.units) run_tile<D, MT, CAP, true>(a, t, 0, 0, ws, -1, sh);
+      }
+      u += k1 - k0;
+      k0 = 0;
+      if (u < end && ++at == n.tiles) {
+        at = 0;
+        if (++h == a.c.heads) {
+          h = 0;
+          rem = 0;
+          ++seq;
+          found = false;
+        }
+      }
+    }
+  }
+  if (threadIdx.x == 0) ws.heads[blockIdx.x] = open;
+}
+
+// Joins the parts of the tile that starts in share blockIdx.x: 256 elements
+// of its rows by 64 lanes, the parts over the waves.
+template <int D, int MT>
+__global__ __launch_bounds__(64 * kWaves) void cache_attention_join_kernel(CacheAttend a, Space ws) {
+  constexpr int R = 16 * MT;
+  __shared__ bq_f32x4 acc[kWaves][64];
+  __shared__ float ml[kWaves][2][64];
+  const int4 open = ws.heads[blockIdx.x];
+  if (open.x == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Seq s = seq_of(a.b, open.y);
+  const int row = (blockIdx.y * 256 + 4 * lane) / D, d = (blockIdx.y * 256 + 4 * lane) % D;
+  const int at = open.w + row;
+  const bool have = at < s.n * a.group;
+  if (open.w + (int)(blockIdx.y * 256) / D >= s.n * a.group) return;
+  float m = -__builtin_inff(), l = 0;
+  bq_f32x4 o = {0, 0, 0, 0};
+  // wave w: parts w, w + 4, ..; each part's sum, scaled to the running maximum
+  if (have)
+    for (int p = wave; p < open.x; p += kWaves) {
+      const int64_t slot = p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p);
+      const float mp = ws.sums[(slot * R + row) * 2], lp = ws.sums[(slot * R + row) * 2 + 1];
+      const bq_f32x4 x = *(const bq_f32x4*)(ws.parts + (slot * R + row) * D + d);
+      const float top = fmaxf(m, mp), f = m == top ? 1.0f : exp2_(m - top), fp = mp == top ? 1.0f : exp2_(mp - top);
+      m = top;
+      l = l * f + lp * fp;
+      o = o * f + x * fp;
+    }
+  acc[wave][lane] = o;
+  ml[wave][0][lane] = m;
+  ml[wave][1][lane] = l;
+  __syncthreads();
+  if (wave || !have) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, ml[w][0][lane]);
+  l = 0;
+  o = (bq_f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const float mw = ml[w][0][lane], f = mw == m ? 1.0f : exp2_(mw - m);
+    l += ml[w][1][lane] * f;
+    o += acc[w][lane] * f;
+  }
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  const int64_t tr = s.row0 + at / a.group;
+  const int head = open.z * a.group + at % a.group;
+  *(bq_u32x2_a2*)(a.out.p + tr * a.out.tok + head * a.out.head + d) =
+      (bq_u32x2){pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)};
+  if (a.lse && d == 0) a.lse[tr * a.q_heads + head] = lse_of(m, l);
+}
+
+// One workgroup a tile. Sequence i's tiles are numbered from starts[i] group /
+// R + i on; the last ones, which see most, go first.
+template <int D, int MT, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_tiles_kernel(CacheAttend a) {
+  constexpr int R = 16 * MT;
+  __shared__ Shared<D, MT> sh;
+  const int64_t v = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
+  const int h = (int)((gridDim.x - 1 - blockIdx.x) % a.c.heads);
+  const auto first = [&](int j) { return (int64_t)start_of(a.b, j) * a.group / R + j; };
+  const int seq = uni(last_upto(a.b.sequences, v, first));
+  Tile t;
+  if (!tile_at<R>(a, seq, uni(seq_of(a.b, seq)), uni((int)(v - first(seq))), h, t)) return;
+  const Span s = span_of(a, t.first, t.last);
+  run_tile<D, MT, CAP, false>(a, t, s.from, s.to, Space{}, -1, sh);
+}
+
+// Rows of a tile and whether a workgroup takes whole tiles: by the mean rows
+// of a sequence and key head, all that the host knows of the lengths.
+struct Form {
+  int mt;
+  bool tiles;
+  int64_t count;  // of tiles, at most
+  int shift;      // of a unit
+};
+Form form_of(const CacheAttend& a, int head_dim) {
+  const int64_t rows = a.b.starts ? ((int64_t)a.b.tokens * a.group + a.b.sequences - 1) / a.b.sequences : a.group;
+  Form f;
+  f.mt = rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
+  f.count = ((int64_t)a.b.tokens * a.group / (16 * f.mt) + a.b.sequences) * a.c.heads;
+  int64_t most = a.b.table_pages << a.c.shift;
+  most = most < kMostTokens ? most : kMostTokens;
+  f.shift = 0;
+  while (f.count * ((most + kStep) / ((int64_t)kStep << f.shift) + 1 + kBegin) >= (int64_t)1 << 30 && f.shift < 23) ++f.shift;
+  f.tiles = a.b.starts && f.mt > 1 && rows > 32 && f.count >= 2 * kShares;
+  return f;
+}
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+Space space_of(void* ws, int mt, int head_dim, size_t* bytes) {
+  const size_t rows = (size_t)2 * kShares * 16 * mt;
+  uint8_t* p = (uint8_t*)ws;
+  const size_t parts = round256(rows * head_dim * 4), sums = round256(rows * 8);
+  *bytes = parts + sums + kShares * sizeof(int4);
+  return {(float*)p, (float*)(p + parts), (int4*)(p + parts + sums)};
+}
+
+template <int D, int MT>
+hipError_t run(const CacheAttend& a, const Form& f, const Space& ws, hipStream_t st) {
+  const dim3 block(64 * kWaves);
+  if constexpr (MT > 1) {
+    if (f.tiles) {
+      if (a.cap > 0) cache_attention_tiles_kernel<D, MT, true><<<(unsigned)f.count, block, 0, st>>>(a);
+      else cache_attention_tiles_kernel<D, MT, false><<<(unsigned)f.count, block, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  }
+  if (a.cap > 0) cache_attention_shares_kernel<D, MT, true><<<kShares, block, 0, st>>>(a, ws, f.shift);
+  else cache_attention_shares_kernel<D, MT, false><<<kShares, block, 0, st>>>(a, ws, f.shift);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int rows = !a.b.starts && a.group < 16 * MT ? a.group : 16 * MT;
+  cache_attention_join_kernel<D, MT><<<dim3(kShares, (rows * D + 255) / 256), block, 0, st>>>(a, ws);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t cache_attention_ws_bytes(const CacheAttend&, int) { return 0; }
+size_t cache_attention_ws_bytes(const CacheAttend& a, int head_dim) {
+  if (!a.b.tokens || !a.b.sequences) return 0;
+  const Form f = form_of(a, head_dim);
+  size_t n = 0;
+  if (!f.tiles) space_of(nullptr, f.mt, head_dim, &n);
+  return n;
+}
 
-hipError_t launch_cache_attention(const CacheAttend& a, int head_dim, void*, hipStream_t st) {
+hipError_t launch_cache_attention(const CacheAttend& a, int head_dim, void* ws, hipStream_t st) {
   if (!a.b.tokens || !a.b.sequences) return hipSuccess;
-  return head_dim == 64 ? run<64>(a, st) : head_dim == 128 ? run<128>(a, st) : run<256>(a, st);
+  const Form f = form_of(a, head_dim);
+  size_t n;
+  const Space s = space_of(ws, f.mt, head_dim, &n);
+  if (f.mt == 1)
+    return head_dim == 64 ? run<64, 1>(a, f, s, st) : head_dim == 128 ? run<128, 1>(a, f, s, st) : run<256, 1>(a, f, s, st);
+  if (f.mt == 2)
+    return head_dim == 64 ? run<64, 2>(a, f, s, st) : head_dim == 128 ? run<128, 2>(a, f, s, st) : run<256, 2>(a, f, s, st);
+  return head_dim == 64 ? run<64, 4>(a, f, s, st) : run<128, 4>(a, f, s, st);
 }
 
 }  // namespace fp8lin

@@ -49,9 +49,9 @@ CacheAttend attend_of(const fp8_cache* c, const fp8_cache_batch* b, int q_heads)
   a.group = q_heads / c->heads;
   return a;
 }
-// its grid: at least a workgroup for each 16 rows
+// its rows are counted with 31 bits
 inline bool attend_fits(const fp8_cache_batch* b, int q_heads) {
-  return batch_fits(b) && (b->tokens * q_heads) / 16 + b->sequences * q_heads < ((int64_t)1 << 31);
+  return batch_fits(b) && (b->tokens + 64 * b->sequences) * q_heads < ((int64_t)1 << 31) - 64;
 }
 
 inline bool fp4_sizes(int64_t K, int64_t N) { return K >= 0 && N >= 0; }
