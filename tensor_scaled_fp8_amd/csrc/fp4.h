@@ -20,7 +20,29 @@ struct Fp4Mat {
 };
 hipError_t launch_fp4_quantize(const uint16_t* w, int64_t ld, const Fp4Mat& q, hipStream_t st);
 hipError_t launch_fp4_dequantize(const Fp4Mat& q, uint16_t* w, int64_t ld, hipStream_t st);
-// Y [x.rows, w.N] = X W of a stored X [M, K]
-hipError_t launch_fp4_linear(const BlockMat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
+
+// X [M, K] quantised (E4M3, a scale for each 128 of a row) in the order that
+// the instructions take it: for each 16 rows and each 128 of K two pieces of
+// 1024 bytes, byte 16 (16 G + r) + i of piece p being element 64 p + 16 G + i
+// of row r; scale bytes [16 rows][4 blocks of 128] as words. The pad of a last
+// part block is zero; rows past the last are not written.
+struct Fp4X {
+  uint8_t *codes, *scales;
+  int64_t M, K;
+};
+__host__ __device__ inline int64_t fp4_xblocks(int64_t K) { return (K + 127) / 128; }
+inline size_t fp4_x_codes(int64_t M, int64_t K) { return (size_t)((M + 15) / 16) * fp4_xblocks(K) * 2048; }
+inline size_t fp4_x_scales(int64_t M, int64_t K) { return (size_t)((M + 15) / 16) * ((fp4_xblocks(K) + 3) / 4) * 64; }
+hipError_t launch_fp4_x(const Bf16Mat& x, const Fp4X& q, hipStream_t st);
+
+// Y [M, N] = X W. Of few rows (and blocks of K) X is quantised by the
+// product's own launch; otherwise it comes quantised. Up to kFp4Few rows the
+// product is of bf16 operands, exact but for FP32 sums, since it waits for W's
+// bytes all the same (64 rows by 4096 x 12288: FEW_64 us; by the 8-bit
+// instructions FEW_64_8); of more, of the 8-bit and 4-bit codes.
+constexpr int64_t kFp4Few = 64;
+bool fp4_fused(int64_t M, int64_t K);
+hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
+hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
 
 }  // namespace fp8lin

@@ -68,7 +68,30 @@ __global__ __launch_bounds__(256) void fp4_dequant_kernel(Fp4Mat q, uint16_t* __
   }
 }
 
+// X quantised for the product: 16 lanes a block of 128, 16 blocks a workgroup
+__global__ __launch_bounds__(256) void fp4_x_kernel(Bf16Mat x, Fp4X q, int nk) {
+  const int t = threadIdx.x, c8 = 8 * (t & 15), r = t >> 4;
+  const int64_t mt = blockIdx.x / nk, row = mt * 16 + r;
+  const int kb = (int)(blockIdx.x % nk);
+  bq_u32x4 v[1];
+  load_rows<1, 1, false>(x, row, (int64_t)kb * kBlk + c8, mt * 16 + 16 <= x.rows && (int64_t)(kb + 1) * kBlk <= x.cols, v);
+  uint2 c[1];
+  uint32_t byte[1];
+  rows_codes<FP8_E4M3>(v, c, byte);
+  if (row >= x.rows) return;
+  uint8_t* o = q.codes + ((mt * nk + kb) * 2 + (c8 >> 6)) * 1024 + ((c8 >> 4 & 3) * 16 + r) * 16 + (c8 & 15);
+  *(uint2*)o = c[0];
+  if (c8 == 0) q.scales[(mt * ((nk + 3) / 4) + (kb >> 2)) * 64 + 4 * r + (kb & 3)] = (uint8_t)byte[0];
+}
+
 }  // namespace
+
+hipError_t launch_fp4_x(const Bf16Mat& x, const Fp4X& q, hipStream_t st) {
+  const int nk = (int)fp4_xblocks(x.cols);
+  if (x.rows == 0 || nk == 0) return hipSuccess;
+  fp4_x_kernel<<<(unsigned)((x.rows + 15) / 16 * nk), 256, 0, st>>>(x, q, nk);
+  return hipGetLastError();
+}
 
 hipError_t launch_fp4_quantize(const uint16_t* w, int64_t ld, const Fp4Mat& q, hipStream_t st) {
   if (q.K == 0 || q.N == 0) return hipSuccess;

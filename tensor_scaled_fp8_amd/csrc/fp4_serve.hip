@@ -1,58 +1,421 @@
-// The linear on a stored 4-bit weight: Y [M, N] = X [M, K] W, X stored in
-// E4M3. A workgroup makes a tile of 16 rows and 16 columns; its waves share
-// out the k-blocks and add their sums over LDS in wave order. The scaled
-// matrix instruction takes W's 4-bit codes and X's 8-bit ones as they are.
+// The linear on a stored 4-bit weight, of few rows: Y [M, N] = X [M, K] W.
+// Bound by the one read of W, which wants every CU's loads in flight:
+//   - a workgroup makes 16 NB columns of Y; its waves share out the blocks of
+//     128 of K and add their FP32 sums over LDS in wave order (the same bits
+//     always);
+//   - a wave loads its share of W to registers, U blocks at a time: a lane's
+//     16 bytes are 32 elements of one column;
+//   - both operands become bf16, exactly (4-bit and 8-bit values times powers
+//     of two), two elements an instruction, the group's scale with them, and
+//     are multiplied by 16x16x32 bf16 products. The 8-bit instructions would
+//     take the codes as they are, but drop bits below 2^-13 of a product's
+//     neighbours, which a later 8-bit rounding (of a key, of the next
+//     linear's input) turns into whole steps: a layer's output was 0.0028
+//     off where its own rounding is 0.0017;
+//   - of one or a few rows (FUSED) every workgroup quantises X itself, into
+//     LDS while its first loads of W fly: one launch, no workspace.
+#include <type_traits>
+
 #include "fp4.h"
 
 namespace fp8lin {
 namespace {
 
+typedef __bf16 f4_bf16x8 __attribute__((ext_vector_type(8)));
+
+template <int N, int I = 0, typename F>
+__device__ inline void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+// a barrier that orders LDS only: global loads stay in flight
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt((63 & 15) | (3 << 14) | (7 << 4) | (0 << 8));  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 8 elements (a word of codes) to bf16
+__device__ inline f4_bf16x8 widen4(uint32_t w, float s) {
+  const bq_u32x4 r = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+  return __builtin_bit_cast(f4_bf16x8, r);
+}
+__device__ inline f4_bf16x8 widen8(uint32_t a, uint32_t b, float s) {
+  return __builtin_bit_cast(f4_bf16x8, uncode8_bf16<FP8_E4M3>(make_uint2(a, b), s));
+}
+
+__device__ inline int64_t w_at(const Fp4Mat& w, int64_t n, int G) {
+  return (n >> 4) * fp4_kblocks(w.K) * 1024 + 256 * G + 16 * (n & 15);
+}
+
+// 64 KB of LDS hold the sums of 8 waves, of up to 8 tiles each
+constexpr int kept_waves(int tiles, int waves) { return tiles * waves > 64 ? waves / 2 : waves; }
+
+// MF: 16-row fragments of X. FUSED: X comes as bf16 x; otherwise quantised, as xq.
+template <bool FUSED, int MF, int NB, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void fp4_few_kernel(Bf16Mat x, Fp4X xq, Fp4Mat w, uint16_t* __restrict__ y, int cols) {
+  // partial sums; FUSED: before them X's values in bf16, rows of `pitch` bytes
+  extern __shared__ uint4 lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, G = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * cols;
+  const int64_t n1 = n0 + cols < w.N ? n0 + cols : w.N;
+  const int nk = (int)fp4_xblocks(w.K);
+  const int k0 = wave * nk / WAVES, k1 = (wave + 1) * nk / WAVES;
+  const int rows = (int)(FUSED ? x.rows : xq.M);
+  const int pitch = nk * 256 + 16;
+  const uint8_t* wrow[NB];
+  const uint8_t* wscale[NB];
+  bool have[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t n = n0 + 16 * b + r16;
+    have[b] = n < n1;
+    wrow[b] = w.codes + w_at(w, n, G);
+    wscale[b] = w.scales + (n >> 4) * (fp4_kblocks(w.K) / 4) * 256 + 64 * G + 4 * (n & 15);
+  }
+  bq_u32x4 wc[U][NB];
+  uint32_t ws[U][NB];
+  bq_f32x4 acc[MF][NB];
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[f][b] = (bq_f32x4){0, 0, 0, 0};
+  auto load_w = [&](int kb, int u) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      wc[u][b] = (bq_u32x4){0, 0, 0, 0};
+      ws[u][b] = 127;
+      if (have[b]) {
+        wc[u][b] = __builtin_nontemporal_load((const bq_u32x4*)(wrow[b] + (int64_t)kb * 1024));
+        ws[u][b] = wscale[b][(int64_t)(kb >> 2) * 256 + (kb & 3)];
+      }
+    }
+  };
+  uint8_t* const l8 = (uint8_t*)lds;
+  if constexpr (FUSED) {
+    // 16 lanes a block of 128, four turns of 4 WAVES blocks at a time; the
+    // first loads are issued before those of W
+    const int blocks = rows * nk, c8 = 8 * (int)(threadIdx.x & 15);
+    constexpr int kTurn = 4 * WAVES;
+    const bool whole = x.cols % kBlk == 0;
+    bq_u32x4 v[4];
+    const int at0 = threadIdx.x >> 4;
+    for (int at = at0; at - at0 < blocks; at += 4 * kTurn) {
+      static_for<4>([&](auto I_) {
+        constexpr int i = decltype(I_)::value;
+        v[i] = (bq_u32x4){0, 0, 0, 0};
+        if (at + kTurn * i < blocks) {
+          const int r = (at + kTurn * i) / nk, c = (at + kTurn * i - r * nk) * kBlk;
+          bq_u32x4 e[1];
+          load_rows<1, 1, false>(x, r, c + c8, whole, e);
+          v[i] = e[0];
+        }
+      });
+      if (at == at0)
+        static_for<U>([&](auto U_) {
+          if (k0 + decltype(U_)::value < k1) load_w(k0 + decltype(U_)::value, decltype(U_)::value);
+        });
+      uint2 q[4];
+      uint32_t byte[4];
+      rows_codes<FP8_E4M3>(v, q, byte);
+      static_for<4>([&](auto I_) {
+        constexpr int i = decltype(I_)::value;
+        const int b = at + kTurn * i;
+        if (b < blocks) {
+          const int r = b / nk;
+          *(bq_u32x4*)(l8 + r * pitch + (b - r * nk) * 256 + 2 * c8) = uncode8_bf16<FP8_E4M3>(q[i], scale_value(byte[i]));
+        }
+      });
+    }
+    lds_barrier();
+  }
+  // this lane's 32 elements 32 G .. of a row's block: the second half of a
+  // piece's lanes hold them in two rows of 16 bytes
+  const int64_t xb = fp4_xblocks(w.K);
+  const uint8_t* xc = FUSED ? nullptr : xq.codes + (G >> 1) * 1024 + (32 * (G & 1) + r16) * 16;
+  const uint8_t* xs = FUSED ? nullptr : xq.scales + 4 * r16;
+  for (int kb = k0; kb < k1; kb += U) {
+    static_for<U>([&](auto U_) {
+      constexpr int u = decltype(U_)::value;
+      if (kb + u < k1 && (!FUSED || kb != k0)) load_w(kb + u, u);
+    });
+    static_for<U>([&](auto U_) {
+      constexpr int u = decltype(U_)::value;
+      if (kb + u < k1) {
+        f4_bf16x8 wf[NB][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) wf[b][j] = widen4(wc[u][b][j], __uint_as_float(ws[u][b] == 255u ? 0x7FC00000u : ws[u][b] << 23));
+        static_for<MF>([&](auto F_) {
+          constexpr int f = decltype(F_)::value;
+          f4_bf16x8 xf[4];
+          if constexpr (FUSED) {
+            bq_u32x4 e[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+            if (r16 < rows) {
+              const uint8_t* p = l8 + r16 * pitch + (kb + u) * 256 + 64 * G;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[j] = *(const bq_u32x4*)(p + 16 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xf[j] = __builtin_bit_cast(f4_bf16x8, e[j]);
+          } else {
+            bq_u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+            uint32_t sx = 127;
+            if (16 * f + r16 < rows) {
+              const uint8_t* p = xc + (f * xb + kb + u) * 2048;
+              lo = *(const bq_u32x4*)p;
+              hi = *(const bq_u32x4*)(p + 256);
+              sx = xs[(f * ((xb + 3) / 4) + ((kb + u) >> 2)) * 64 + ((kb + u) & 3)];
+            }
+            const float s = scale_value(sx);
+            xf[0] = widen8(lo.x, lo.y, s);
+            xf[1] = widen8(lo.z, lo.w, s);
+            xf[2] = widen8(hi.x, hi.y, s);
+            xf[3] = widen8(hi.z, hi.w, s);
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[f][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b][j], xf[j], acc[f][b], 0, 0, 0);
+        });
+      }
+    });
+  }
+  if constexpr (FUSED) lds_barrier();  // X's values are read
+  bq_f32x4* const part = (bq_f32x4*)lds;
+  constexpr int S = kept_waves(MF * NB, WAVES);  // waves whose sums LDS holds at once
+  if constexpr (S < WAVES) {
+    // the upper half's sums first, into the lower half's
+    if (wave >= S) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) part[((wave - S) * MF * NB + f * NB + b) * 64 + lane] = acc[f][b];
+    }
+    lds_barrier();
+    if (wave < S) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[f][b] += part[(wave * MF * NB + f * NB + b) * 64 + lane];
+    }
+    lds_barrier();
+  }
+  if (wave < S) {
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) part[(wave * MF * NB + f * NB + b) * 64 + lane] = acc[f][b];
+  }
+  lds_barrier();
+  for (int i = wave; i < MF * NB; i += WAVES) {
+    const int row = 16 * (i / NB) + r16;
+    bq_f32x4 s = part[i * 64 + lane];
+#pragma unroll
+    for (int k = 1; k < S; ++k) s += part[(k * MF * NB + i) * 64 + lane];
+    // this lane: columns 4 G .. 4 G + 3 of column block i % NB
+    const int64_t n = n0 + 16 * (i % NB) + 4 * G;
+    if (row >= rows) continue;
+    uint16_t* d = y + row * w.N + n;
+    const bq_u32x2 v = {pack_bf16(s.x, s.y), pack_bf16(s.z, s.w)};
+    if (n + 4 <= n1) *(bq_u32x2_a2*)d = v;
+    else
+      for (int k = 0; k < 4 && n + k < n1; ++k) d[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+  }
+}
+
+template <bool FUSED, int MF, int NB, int U>
+hipError_t run(const Bf16Mat& x, const Fp4X& xq, const Fp4Mat& w, uint16_t* y, int cols, hipStream_t st) {
+  constexpr int kWaves = 8;
+  size_t lds = 1024 * kept_waves(MF * NB, kWaves) * MF * NB;
+  if (FUSED) {
+    const size_t values = (size_t)x.rows * (fp4_xblocks(w.K) * 256 + 16);
+    if (values > lds) lds = values;
+  }
+  fp4_few_kernel<FUSED, MF, NB, kWaves, U>
+      <<<dim3((unsigned)((w.N + cols - 1) / cols)), 64 * kWaves, lds, st>>>(x, xq, w, y, cols);
+  return hipGetLastError();
+}
+
+// Columns of Y a workgroup makes: all 256 CUs get one workgroup (or C) of
+// equal work, since a CU streams from HBM at no more than its share, 20 GB/s.
+// At most `most`, what the accumulators of a wave are laid out for.
+inline int part_cols(int64_t N, int most) {
+  const int64_t c = (N + 256 * most - 1) / (256 * most);
+  return (int)((N + 256 * c - 1) / (256 * c));
+}
+
+// Of more rows: a workgroup's tile is 16 MF rows by 64 NB columns. Its four
+// waves have 16 NB columns each, whose codes go from memory to registers in
+// the instruction's order; X's tile goes over LDS, a block of 128 of K at a
+// time in turn with the one before. The scaled instruction takes 4-bit and
+// 8-bit codes as they are.
 typedef int f4_v8i __attribute__((ext_vector_type(8)));
 
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void fp4_serve_kernel(BlockMat x, Fp4Mat w, uint16_t* __restrict__ y) {
-  __shared__ bq_f32x4 part[WAVES][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, G = lane >> 4;
-  const int64_t panel = blockIdx.x, row = (int64_t)blockIdx.y * 16 + r, kblocks = fp4_kblocks(w.K);
-  const uint8_t* wc = w.codes + panel * kblocks * 1024 + 16 * lane;
-  const uint8_t* ws = w.scales + panel * (kblocks / 4) * 256 + 4 * lane;
-  const bool mine = row < x.rows;
-  const uint8_t* xc = x.codes + row * x.pitch + 16 * G;
-  const uint8_t* xs = x.scales + scale_pos(row);
-  const int nk = (int)(x.pitch / kBlk);
-  bq_f32x4 acc = {0, 0, 0, 0};
-  for (int kb = wave; kb < nk; kb += WAVES) {
-    const bq_u32x4 c = *(const bq_u32x4*)(wc + (int64_t)kb * 1024);
-    const uint32_t sw = ws[(int64_t)(kb >> 2) * 256 + (kb & 3)];
-    bq_u32x4 p = {0, 0, 0, 0}, q = {0, 0, 0, 0};
-    uint32_t sx = 127;
-    if (mine) {
-      p = *(const bq_u32x4*)(xc + (int64_t)kb * kBlk);
-      q = *(const bq_u32x4*)(xc + (int64_t)kb * kBlk + 64);
-      sx = xs[(int64_t)kb * x.srows];
-    }
-    const f4_v8i e = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
-    const f4_v8i a = {(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(e, a, acc, 4, 0, 0, (int)sw, 0, (int)sx);
+template <int MF, int NB>
+__global__ __launch_bounds__(256) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_t* __restrict__ y, int tiles_n) {
+  constexpr int kPieces = 2 * MF, kTurns = (kPieces + 3) / 4;  // of 1024 bytes; each wave's
+  __shared__ bq_u32x4 xl[2][kPieces][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, G = lane >> 4;
+  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * MF;  // in 16 rows
+  const int64_t p0 = ((int64_t)(blockIdx.x % tiles_n) * 4 + wave) * NB;
+  const int64_t panels = (w.N + 15) / 16, mtiles = (x.M + 15) / 16;
+  const int nk = (int)fp4_xblocks(x.K);
+  const int64_t kb4 = fp4_kblocks(w.K), xk4 = (nk + 3) / 4;
+  const uint8_t *wc[NB], *ws[NB], *xs[MF], *xc[kTurns];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t p = p0 + b < panels ? p0 + b : panels - 1;  // a column past the last is computed and not stored
+    wc[b] = w.codes + p * kb4 * 1024 + 16 * lane;
+    ws[b] = w.scales + p * (kb4 / 4) * 256 + 4 * lane;
   }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave || !mine) return;
 #pragma unroll
-  for (int i = 1; i < WAVES; ++i) acc += part[i][lane];
-  const int64_t n = panel * 16 + 4 * G;
+  for (int f = 0; f < MF; ++f) {
+    const int64_t m = m0 + f < mtiles ? m0 + f : mtiles - 1;
+    xs[f] = x.scales + m * xk4 * 64 + 4 * r16;
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (n + k < w.N) y[row * w.N + n + k] = (uint16_t)pack_bf16(acc[k], 0.0f);
+  for (int i = 0; i < kTurns; ++i) {
+    const int c = wave + 4 * i < kPieces ? wave + 4 * i : kPieces - 1;
+    const int64_t m = m0 + c / 2 < mtiles ? m0 + c / 2 : mtiles - 1;
+    xc[i] = x.codes + m * nk * 2048 + (c & 1) * 1024 + 16 * lane;
+  }
+  bq_f32x4 acc[MF][NB];
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[f][b] = (bq_f32x4){0, 0, 0, 0};
+  bq_u32x4 xv[kTurns], wv[4][NB];
+  uint32_t wsv[NB], xsv[MF];
+  const auto load_x = [&](int kb) {
+    const int k = kb < nk ? kb : nk - 1;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) xv[i] = *(const bq_u32x4*)(xc[i] + (int64_t)k * 2048);
+  };
+  const auto store_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+      if (wave + 4 * i < kPieces) xl[buf][wave + 4 * i][lane] = xv[i];
+  };
+  const auto load_w = [&](int kb, bq_u32x4 (&v)[NB]) {
+    const int k = kb < nk ? kb : nk - 1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) v[b] = *(const bq_u32x4*)(wc[b] + (int64_t)k * 1024);
+  };
+  load_x(0);
+  load_w(0, wv[0]);
+  load_w(1, wv[1]);
+  load_w(2, wv[2]);
+  store_x(0);
+  load_x(1);
+  lds_barrier();
+  for (int k4 = 0; k4 < nk; k4 += 4) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wsv[b] = *(const uint32_t*)(ws[b] + (int64_t)(k4 >> 2) * 256);
+#pragma unroll
+    for (int f = 0; f < MF; ++f) xsv[f] = *(const uint32_t*)(xs[f] + (int64_t)(k4 >> 2) * 64);
+    static_for<4>([&](auto I_) {
+      constexpr int i = decltype(I_)::value;
+      const int kb = k4 + i;
+      if (kb < nk) {
+        load_w(kb + 3, wv[(i + 3) & 3]);
+        static_for<MF>([&](auto F_) {
+          constexpr int f = decltype(F_)::value;
+          const bq_u32x4 p = xl[i & 1][2 * f][lane], q = xl[i & 1][2 * f + 1][lane];
+          const f4_v8i e = {(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
+          static_for<NB>([&](auto B_) {
+            constexpr int b = decltype(B_)::value;
+            const bq_u32x4 c = wv[i][b];
+            const f4_v8i a = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+            acc[f][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, e, acc[f][b], 4, 0, i, (int)wsv[b], i, (int)xsv[f]);
+          });
+        });
+        store_x((i + 1) & 1);
+        load_x(kb + 2);
+        lds_barrier();
+      }
+    });
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int64_t row = (m0 + f) * 16 + r16;
+    if (row >= x.M) continue;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int64_t n = (p0 + b) * 16 + 4 * G;
+      uint16_t* d = y + row * w.N + n;
+      const bq_u32x2 v = {pack_bf16(acc[f][b].x, acc[f][b].y), pack_bf16(acc[f][b].z, acc[f][b].w)};
+      if (n + 4 <= w.N) *(bq_u32x2_a2*)d = v;
+      else
+        for (int k = 0; k < 4 && n + k < w.N; ++k) d[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+template <int MF, int NB>
+hipError_t run_many(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
+  const int64_t tm = ((x.M + 15) / 16 + MF - 1) / MF, tn = (w.N + 64 * NB - 1) / (64 * NB);
+  fp4_many_kernel<MF, NB><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
+  return hipGetLastError();
+}
+template <int MF>
+hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, int nb, uint16_t* y, hipStream_t st) {
+  return nb == 1 ? run_many<MF, 1>(x, w, y, st) : nb == 2 ? run_many<MF, 2>(x, w, y, st) : run_many<MF, 3>(x, w, y, st);
 }
 
 }  // namespace
 
-hipError_t launch_fp4_linear(const BlockMat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
+// X's values in bf16 fit 64 KB of LDS
+bool fp4_fused(int64_t M, int64_t K) { return M <= 16 && M * fp4_xblocks(K) <= 248; }
+
+hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
   if (x.rows == 0 || w.N == 0) return hipSuccess;
-  fp4_serve_kernel<4><<<dim3((unsigned)((w.N + 15) / 16), (unsigned)((x.rows + 15) / 16)), 256, 0, st>>>(x, w, y);
-  return hipGetLastError();
+  const Fp4X none = {nullptr, nullptr, 0, 0};
+  const int cols = part_cols(w.N, 48);
+  return cols <= 16   ? run<true, 1, 1, 4>(x, none, w, y, cols, st)
+         : cols <= 32 ? run<true, 1, 2, 4>(x, none, w, y, cols, st)
+                      : run<true, 1, 3, 4>(x, none, w, y, cols, st);
+}
+
+hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
+  if (x.M == 0 || w.N == 0) return hipSuccess;
+  if (x.M <= kFp4Few) {
+    const Bf16Mat none = {nullptr, 0, 0, 0};
+    const int cols = part_cols(w.N, 48), mf = x.M <= 16 ? 1 : x.M <= 32 ? 2 : 4, nb = cols <= 16 ? 1 : cols <= 32 ? 2 : 3;
+#define FEW(m, n) \
+  if (mf == m && nb == n) return run<false, m, n, (m > 2 ? 2 : 4)>(none, x, w, y, cols, st);
+    FEW(1, 1) FEW(1, 2) FEW(1, 3) FEW(2, 1) FEW(2, 2) FEW(2, 3) FEW(4, 1) FEW(4, 2) FEW(4, 3)
+#undef FEW
+  }
+  // the tile whose rounds of 256 workgroups have the least products in all
+  const int64_t mt = (x.M + 15) / 16, panels = (w.N + 15) / 16;
+  int best_mf = 4, best_nb = 1;
+  double least = 0;
+  for (int mf = 4; mf <= 8; ++mf)
+    for (int nb = 1; nb <= 3; ++nb) {
+      const int64_t groups = (mt + mf - 1) / mf * ((panels + 4 * nb - 1) / (4 * nb));
+      // 4 + products: what a block of K costs a wave besides them
+      const double cost = (double)((groups + 255) / 256) * (mf * nb + 4);
+      if (least == 0 || cost < least) least = cost, best_mf = mf, best_nb = nb;
+    }
+  switch (best_mf) {
+    case 4: return run_rows<4>(x, w, best_nb, y, st);
+    case 5: return run_rows<5>(x, w, best_nb, y, st);
+    case 6: return run_rows<6>(x, w, best_nb, y, st);
+    case 7: return run_rows<7>(x, w, best_nb, y, st);
+    default: return run_rows<8>(x, w, best_nb, y, st);
+  }
 }
 
 }  // namespace fp8lin

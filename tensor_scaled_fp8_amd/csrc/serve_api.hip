@@ -56,17 +56,19 @@ inline bool attend_fits(const fp8_cache_batch* b, int q_heads) {
 
 inline bool fp4_sizes(int64_t K, int64_t N) { return K >= 0 && N >= 0; }
 inline bool fp4_fits(int64_t K, int64_t N) { return K <= (1 << 20) && N <= ((int64_t)1 << 23); }
-// X's scales are addressed with 31 bits
+// X's blocks of 16 rows by 128 are counted with 31 bits
 inline bool fp4_rows_fit(int64_t M, int64_t K) {
-  return M <= (1 << 19) && round_blk(M) * (round_blk(K) / kBlk) < ((int64_t)1 << 31);
+  return M <= (1 << 22) && (M + 15) / 16 * fp4_xblocks(K) < ((int64_t)1 << 31);
 }
+// and so are the product's tiles
+inline bool fp4_product_fits(int64_t M, int64_t N) { return (M / 64 + 1) * (N / 64 + 1) < ((int64_t)1 << 31); }
 struct Fp4Scratch {
-  BlockMat x;
+  Fp4X x;
   size_t bytes;
   Fp4Scratch(void* p, int64_t M, int64_t K) {
-    const size_t codes = ((size_t)M * round_blk(K) + 255) / 256 * 256;
-    x = {(uint8_t*)p, p ? (uint8_t*)p + codes : nullptr, round_blk(K), round_blk(M), M, K};
-    bytes = codes + (size_t)round_blk(M) * (round_blk(K) / kBlk);
+    const size_t codes = fp4_x_codes(M, K);  // a multiple of 2048
+    x = {(uint8_t*)p, p ? (uint8_t*)p + codes : nullptr, M, K};
+    bytes = codes + fp4_x_scales(M, K);
   }
 };
 
@@ -159,7 +161,8 @@ fp8_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t K
 }
 
 size_t fp4_linear_bytes(int64_t M, int64_t K, int64_t N) {
-  return M <= 0 || K <= 0 || N <= 0 || !fp4_fits(K, N) || !fp4_rows_fit(M, K) ? 0 : Fp4Scratch(nullptr, M, K).bytes;
+  if (M <= 0 || K <= 0 || N <= 0 || !fp4_fits(K, N) || !fp4_rows_fit(M, K) || fp4_fused(M, K)) return 0;
+  return Fp4Scratch(nullptr, M, K).bytes;
 }
 
 fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
@@ -168,14 +171,16 @@ fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t 
       !aligned(scratch, 16) || !aligned(Y, 2))
     return FP8_ERR_INVALID;
   if ((M && K && !X) || (K && N && (!codes || !scales)) || (M && N && !Y)) return FP8_ERR_INVALID;
-  if (!fp4_fits(K, N) || !fp4_rows_fit(M, K)) return FP8_ERR_UNSUPPORTED;
+  if (!fp4_fits(K, N) || !fp4_rows_fit(M, K) || !fp4_product_fits(M, N)) return FP8_ERR_UNSUPPORTED;
   const size_t need = fp4_linear_bytes(M, K, N);
   if (need && (!scratch || scratch_bytes < need)) return FP8_ERR_INVALID;
+  const Bf16Mat x = {(const uint16_t*)X, ldx, M, K};
+  const Fp4Mat w = {(uint8_t*)codes, (uint8_t*)scales, K, N};
+  if (fp4_fused(M, K)) return hip_status(launch_fp4_fused(x, w, (uint16_t*)Y, stream));
   const Fp4Scratch s(scratch, M, K);
-  const BlockMat none = {nullptr, nullptr, 0, 0, 0, 0};
-  const hipError_t e = launch_block_quantize({(const uint16_t*)X, ldx, M, K}, FP8_E4M3, s.x, none, 0, stream);
+  const hipError_t e = launch_fp4_x(x, s.x, stream);
   if (e != hipSuccess) return FP8_ERR_HIP;
-  return hip_status(launch_fp4_linear(s.x, {(uint8_t*)codes, (uint8_t*)scales, K, N}, (uint16_t*)Y, stream));
+  return hip_status(launch_fp4_linear(s.x, w, (uint16_t*)Y, stream));
 }
 
 }  // extern "C"
