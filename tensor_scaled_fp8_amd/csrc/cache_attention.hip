@@ -37,6 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 
 typedef __bf16 ca_bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 ca_bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t ca_u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ inline uint32_t bf16_of2(uint32_t w, float s, bool hi) {
@@ -170,6 +171,20 @@ __device__ inline void load_codes(const CacheAttend& a, const Blocks& bl, int n,
     for (int i = 0; i < D / 64; ++i) c.w[b][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off + 1024 * i, 0, 0);
   }
 }
+// How a product of a query and a key becomes a weight's exponent: times unit,
+// after tanh with a cap. A negative scale's sign goes to the queries, and of a
+// scale of 0 they are 0, so that unit is above 0 and the largest score is the
+// largest product's.
+struct Scores {
+  float unit, per_cap, cap_log2;
+  uint32_t flip, keep;  // of the queries' bits
+};
+__device__ inline Scores scores_of(const CacheAttend& a, bool cap) {
+  const float scale = a.scale == 0 ? 1.0f : __builtin_fabsf(a.scale);
+  return {cap ? 1.0f : scale * kLog2e, cap ? scale / a.cap : 0.0f, cap ? a.cap * kLog2e : 0.0f,
+          a.scale < 0 ? 0x80008000u : 0u, a.scale == 0 ? 0u : 0xFFFFFFFFu};
+}
+
 // Step n's scales
 struct Scales {
   float k[2], v[2];
@@ -194,81 +209,98 @@ struct Queries {
   __device__ ca_bf16x8 get(int, int i) const { return f[i]; }
 };
 
-// 32 tokens from j0 into a wave's state; pos: the positions of the lane's rows
-// (-1: no row). next_k, next_v issue the next step's loads, as soon as this
-// one's codes are used.
+// 32 tokens from j0 into a wave's state. hard: some of them are hidden from
+// some rows (pos: the positions of the lane's rows; -1: no row). next_k,
+// next_v issue the next step's loads, as soon as this one's codes are used.
 template <int D, int MT, bool CAP, bool FINE, typename Q, typename NextK, typename NextV>
-__device__ inline void attend_group(const CacheAttend& a, const Tile& t, int j0, const int (&pos)[MT], const Q& query,
-                                    int g, const Scales& sc, Codes<D>& k, Codes<D>& c, State<D, MT>& st, NextK next_k,
+__device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int j0, bool hard, const int (&pos)[MT], const Q& query,
+                                    int g, const Scales& s8, Codes<D>& k, Codes<D>& c, State<D, MT>& st, NextK next_k,
                                     NextV next_v) {
   constexpr int P = D / 64;
-  // hidden from somebody: the rows' positions are first .. last
-  const bool hard = !sc.there[0] | !sc.there[1] | (j0 + 31 > t.first) | ((a.window > 0) & (j0 <= t.last - a.window));
-  const float unit = CAP ? a.scale : a.scale * kLog2e;
-  const auto key = [&](int b, int i) {
-    const ca_u32x4 w = k.w[b][i / 2];
-    return i & 1 ? widen(w.z, sc.k[b], w.w, sc.k[b]) : widen(w.x, sc.k[b], w.y, sc.k[b]);
-  };
-  ca_bf16x8 kf[2][MT > 1 ? 2 * P : 1];  // one row tile takes them as they are widened
-  if constexpr (MT > 1) {
+  bq_f32x4 x[MT][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+  for (int r = 0; r < MT; ++r) x[r][0] = x[r][1] = (bq_f32x4){0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 2 * P; ++i) kf[b][i] = key(b, i);
-    next_k();
+  for (int i = 0; i < 2 * P; ++i) {
+    const ca_u32x4 w0 = k.w[0][i / 2], w1 = k.w[1][i / 2];
+    const ca_bf16x8 k0 = i & 1 ? widen(w0.z, s8.k[0], w0.w, s8.k[0]) : widen(w0.x, s8.k[0], w0.y, s8.k[0]);
+    const ca_bf16x8 k1 = i & 1 ? widen(w1.z, s8.k[1], w1.w, s8.k[1]) : widen(w1.x, s8.k[1], w1.y, s8.k[1]);
+#pragma unroll
+    for (int r = 0; r < MT; ++r) {
+      const ca_bf16x8 q = query.get(r, i);
+      x[r][0] = mma(k0, q, x[r][0]);
+      x[r][1] = mma(k1, q, x[r][1]);
+    }
+  }
+  next_k();
+  if constexpr (CAP) {
+#pragma unroll
+    for (int r = 0; r < MT; ++r)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[r][b][i] = sc.cap_log2 * tanh_(x[r][b][i] * sc.per_cap);
   }
   uint32_t seen[MT];  // bit i: the row sees token i of the lane's 8
-  ca_bf16x8 pf[MT], pl[FINE ? MT : 1];
+  if (hard) {
+    asm volatile("");  // a branch: every step would pay for the selects
 #pragma unroll
-  for (int r = 0; r < MT; ++r) {
-    float s[8];
-    bq_f32x4 x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 2 * P; ++i) {
-      const ca_bf16x8 q = query.get(r, i);
-      x0 = mma(MT > 1 ? kf[0][MT > 1 ? i : 0] : key(0, i), q, x0);
-      x1 = mma(MT > 1 ? kf[1][MT > 1 ? i : 0] : key(1, i), q, x1);
-    }
-    if constexpr (MT == 1) next_k();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[i] = (i < 4 ? x0[i & 3] : x1[i & 3]) * unit;
-      if constexpr (CAP) s[i] = a.cap * kLog2e * tanh_(s[i] / a.cap);
-    }
-    if (hard) {
+    for (int r = 0; r < MT; ++r) {
       seen[r] = 0;
       const int low = a.window > 0 ? pos[r] - a.window : -1;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        const bool is = sc.there[i >> 2] & (j <= pos[r]) & (j > low);
+        const bool is = s8.there[i >> 2] & (j <= pos[r]) & (j > low);
         seen[r] |= is ? 1u << i : 0u;
-        if (!is) s[i] = -__builtin_inff();
+        if (!is) x[r][i >> 2][i & 3] = -__builtin_inff();
       }
     }
-    const float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-    if (__any(top > st.m[r] + kSlack)) {
-      const float m = fmaxf(quad_max(top), st.m[r]);
+  }
+  float top[MT];
+  bool over = false;
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    top[r] = fmaxf(fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3])),
+                   fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3]))) * sc.unit;
+    over |= top[r] > st.m[r] + kSlack;
+  }
+  if (__any(over)) {
+#pragma unroll
+    for (int r = 0; r < MT; ++r) {
+      const float m = fmaxf(quad_max(top[r]), st.m[r]);
       const float f = m == st.m[r] ? 1.0f : exp2_(st.m[r] - m);
       st.m[r] = m;
       st.l[r] *= f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) st.o[r][i] *= f;
     }
+  }
+  ca_bf16x8 pf[MT], pl[FINE ? MT : 1];
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
     const float base = st.m[r] == -__builtin_inff() ? 0.0f : st.m[r];
     float p[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = exp2_(s[i] - base);
-    st.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    ca_u32x4 w, x;
+    for (int i = 0; i < 8; ++i) p[i] = exp2_(__builtin_fmaf(x[r][i >> 2][i & 3], sc.unit, -base));
+    ca_u32x4 w, y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       w[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
       if constexpr (FINE)
-        x[i] = pack_bf16(p[2 * i] - __uint_as_float(w[i] << 16), p[2 * i + 1] - __uint_as_float(high_half(w[i])));
+        y[i] = pack_bf16(p[2 * i] - __uint_as_float(w[i] << 16), p[2 * i + 1] - __uint_as_float(high_half(w[i])));
     }
     pf[r] = __builtin_bit_cast(ca_bf16x8, w);
-    if constexpr (FINE) pl[r] = __builtin_bit_cast(ca_bf16x8, x);
+    if constexpr (FINE) {
+      pl[r] = __builtin_bit_cast(ca_bf16x8, y);
+      st.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    } else {
+      // of the rounded weights, two an instruction
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st.l[r] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(ca_bf16x2, w[i]),
+                                                  __builtin_bit_cast(ca_bf16x2, 0x3F803F80u), st.l[r], false);
+    }
   }
   if (hard) {
     // a hidden token's weight is 0, but a NaN times 0 is one: the NaNs are
@@ -279,7 +311,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Tile& t, int j0,
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) any |= nan_bytes(c.w[b][i][k]);
+        for (int n = 0; n < 4; ++n) any |= nan_bytes(c.w[b][i][n]);
     if (__any(any != 0)) {
       // found anew: 32 registers less than held from the search
 #pragma unroll
@@ -298,18 +330,18 @@ __device__ inline void attend_group(const CacheAttend& a, const Tile& t, int j0,
         for (int r = 0; r < MT; ++r) {
           ca_u32x4 w;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = (seen[r] >> (2 * k) & 1u) * 0x3F80u | (seen[r] >> (2 * k + 1) & 1u) * 0x3F800000u;
-          const bq_f32x4 x = mma(nf, __builtin_bit_cast(ca_bf16x8, w), (bq_f32x4){0, 0, 0, 0});
+          for (int e = 0; e < 4; ++e) w[e] = (seen[r] >> (2 * e) & 1u) * 0x3F80u | (seen[r] >> (2 * e + 1) & 1u) * 0x3F800000u;
+          const bq_f32x4 y = mma(nf, __builtin_bit_cast(ca_bf16x8, w), (bq_f32x4){0, 0, 0, 0});
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (x[k] > 0) st.o[r][i][k] = nan();
+          for (int e = 0; e < 4; ++e)
+            if (y[e] > 0) st.o[r][i][e] = nan();
         }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    const ca_bf16x8 vf = widen(c.w[0][i / 4][i % 4], sc.v[0], c.w[1][i / 4][i % 4], sc.v[1]);
+    const ca_bf16x8 vf = widen(c.w[0][i / 4][i % 4], s8.v[0], c.w[1][i / 4][i % 4], s8.v[1]);
 #pragma unroll
     for (int r = 0; r < MT; ++r) {
       st.o[r][i] = mma(vf, pf[r], st.o[r][i]);
@@ -340,11 +372,12 @@ struct LdsQueries {
 };
 
 template <int D>
-__device__ inline ca_u32x4 query_at(const CacheAttend& a, const Tile& t, int row, int i, int g) {
+__device__ inline ca_u32x4 query_at(const CacheAttend& a, const Scores& sc, const Tile& t, int row, int i, int g) {
   if (row >= t.s.n * a.group) return (ca_u32x4){0, 0, 0, 0};
   const int tok = row / a.group, head = t.h * a.group + row % a.group;
-  return *(const bq_u32x4_a2*)(a.q.p + (int64_t)(t.s.row0 + tok) * a.q.tok + head * a.q.head + 64 * (i / 2) + 16 * g +
-                               8 * (i % 2));
+  const ca_u32x4 w = *(const bq_u32x4_a2*)(a.q.p + (int64_t)(t.s.row0 + tok) * a.q.tok + head * a.q.head + 64 * (i / 2) +
+                                           16 * g + 8 * (i % 2));
+  return (w ^ sc.flip) & sc.keep;
 }
 
 // The waves' sums (their maxima and sums are in sh.ml already) joined and written
@@ -415,7 +448,8 @@ __device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& 
 template <int D, int MT, bool CAP, bool FINE>
 __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t from, int64_t to, const Space& ws, int slot,
                                 Shared<D, MT>& sh) {
-  constexpr int R = 16 * MT, W = D / 16, C = W < 8 ? W : 8;
+  constexpr int W = D / 16;
+  const Scores sc = scores_of(a, CAP);
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));  // nothing is held from tile to tile
   const int wave = uni((int)(threadIdx.x >> 6));
@@ -440,10 +474,10 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
   Queries<D, MT> mine;
   if constexpr (MT == 1) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) mine.f[i] = __builtin_bit_cast(ca_bf16x8, query_at<D>(a, t, t.r0 + lo16, i, g));
+    for (int i = 0; i < D / 32; ++i) mine.f[i] = __builtin_bit_cast(ca_bf16x8, query_at<D>(a, sc, t, t.r0 + lo16, i, g));
   } else {
     for (int n = wave; n < MT * (D / 32); n += kWaves)
-      sh.q[n / (D / 32)][n % (D / 32)][lane] = query_at<D>(a, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
+      sh.q[n / (D / 32)][n % (D / 32)][lane] = query_at<D>(a, sc, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
     __syncthreads();
   }
   Codes<D> k, v;
@@ -454,10 +488,12 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
     const bool more = n + 1 < steps;
     const auto next_k = [&] { load_codes<D, false>(a, bl, next, more, lane, k); };
     const auto next_v = [&] { load_codes<D, true>(a, bl, next, more, lane, v); };
-    const Scales sc = scales_of(bl, n & 31);
+    const Scales s8 = scales_of(bl, n & 31);
     if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * kStep, to, lane);
-    if constexpr (MT == 1) attend_group<D, MT, CAP, FINE>(a, t, j0, pos, mine, g, sc, k, v, st, next_k, next_v);
-    else attend_group<D, MT, CAP, FINE>(a, t, j0, pos, LdsQueries<D, MT>{sh, lane}, g, sc, k, v, st, next_k, next_v);
+    // hidden from somebody: the rows' positions are first .. last
+    const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && j0 <= t.last - a.window)));
+    if constexpr (MT == 1) attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, mine, g, s8, k, v, st, next_k, next_v);
+    else attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, LdsQueries<D, MT>{sh, lane}, g, s8, k, v, st, next_k, next_v);
   }
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
