@@ -57,6 +57,8 @@ __device__ inline float nan() { return __uint_as_float(0x7FC00000u); }
 
 __device__ inline uint32_t high_half(uint32_t w) { return w & 0xFFFF0000u; }
 
+__device__ inline float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // over the four lanes that share lane % 16
 __device__ inline float quad_max(float a) {
   a = fmaxf(a, __shfl_xor(a, 16));
@@ -147,8 +149,8 @@ struct Blocks {
   uint32_t lo, hi;  // its number; hi < 0: it is not there
   uint32_t scales;  // bytes of K and V
 };
-__device__ inline Blocks blocks_of(const CacheAttend& a, const Tile& t, int64_t j, int64_t to, int lane) {
-  j += (lane >> 1) * kStep + 16 * (lane & 1);
+__device__ inline Blocks blocks_of(const CacheAttend& a, const Tile& t, int64_t j, int64_t to, int step, int lane) {
+  j += (lane >> 1) * step + 16 * (lane & 1);
   const int64_t blk = j < to ? block_at(a.c, a.b, t.seq, j, t.h) : -1;
   Blocks b = {(uint32_t)blk, (uint32_t)(blk >> 32), 127u | 127u << 8};
   if (blk >= 0) b.scales = *(const uint16_t*)(a.c.scales + 2 * blk);
@@ -243,15 +245,16 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
   }
   uint32_t seen[MT];  // bit i: the row sees token i of the lane's 8
   if (hard) {
-    asm volatile("");  // a branch: every step would pay for the selects
 #pragma unroll
     for (int r = 0; r < MT; ++r) {
       seen[r] = 0;
-      const int low = a.window > 0 ? pos[r] - a.window : -1;
+      int at = pos[r];
+      asm volatile("" : "+v"(at));  // computed here: every step would pay for the selects
+      const int low = a.window > 0 ? at - a.window : -1;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        const bool is = s8.there[i >> 2] & (j <= pos[r]) & (j > low);
+        const bool is = s8.there[i >> 2] & (j <= at) & (j > low);
         seen[r] |= is ? 1u << i : 0u;
         if (!is) x[r][i >> 2][i & 3] = -__builtin_inff();
       }
@@ -261,8 +264,9 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
   bool over = false;
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
-    top[r] = fmaxf(fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3])),
-                   fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3]))) * sc.unit;
+    // a NaN stays one: its row's sum will be, whatever the maximum
+    top[r] = larger(larger(larger(x[r][0][0], x[r][0][1]), larger(x[r][0][2], x[r][0][3])),
+                    larger(larger(x[r][1][0], x[r][1][1]), larger(x[r][1][2], x[r][1][3]))) * sc.unit;
     over |= top[r] > st.m[r] + kSlack;
   }
   if (__any(over)) {
@@ -351,6 +355,27 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
   next_v();
 }
 
+// `steps` times 32 tokens, from j on every `step`, into a wave's state
+template <int D, int MT, bool CAP, bool FINE, typename Q>
+__device__ inline void walk(const CacheAttend& a, const Scores& sc, const Tile& t, int64_t j, int64_t to, int step, int steps,
+                            const int (&pos)[MT], const Q& query, int lane, State<D, MT>& st) {
+  Blocks bl = blocks_of(a, t, j, to, step, lane);
+  Codes<D> k, v;
+  load_codes<D, false>(a, bl, 0, steps > 0, lane, k);
+  load_codes<D, true>(a, bl, 0, steps > 0, lane, v);
+  for (int n = 0; n < steps; ++n) {
+    const int j0 = (int)(j + (int64_t)n * step), next = (n + 1) & 31;
+    const bool more = n + 1 < steps;
+    const auto next_k = [&] { load_codes<D, false>(a, bl, next, more, lane, k); };
+    const auto next_v = [&] { load_codes<D, true>(a, bl, next, more, lane, v); };
+    const Scales s8 = scales_of(bl, n & 31);
+    if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * step, to, step, lane);
+    // hidden from somebody: the rows' positions are first .. last
+    const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && j0 <= t.last - a.window)));
+    attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, query, lane >> 4, s8, k, v, st, next_k, next_v);
+  }
+}
+
 // Where a tile's part goes: parts[slot][row][D] and the row's maximum and sum
 struct Space {
   float* parts;
@@ -364,11 +389,11 @@ struct Shared {
   float ml[kWaves][2][16 * MT];
   ca_u32x4 q[MT > 1 ? MT : 1][MT > 1 ? D / 32 : 1][MT > 1 ? 64 : 1];
 };
-template <int D, int MT>
+template <int D>
 struct LdsQueries {
-  const Shared<D, MT>& s;
+  const ca_u32x4* q;  // [16 rows][D / 32][lane]
   int lane;
-  __device__ ca_bf16x8 get(int r, int i) const { return __builtin_bit_cast(ca_bf16x8, s.q[r][i][lane]); }
+  __device__ ca_bf16x8 get(int r, int i) const { return __builtin_bit_cast(ca_bf16x8, q[(r * (D / 32) + i) * 64 + lane]); }
 };
 
 template <int D>
@@ -459,7 +484,6 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
   to = uni(to);
   const int64_t j = from + wave * kGroup;
   const int steps = j < to ? (int)((to - j + kStep - 1) / kStep) : 0;
-  Blocks bl = blocks_of(a, t, j, to, lane);
   int pos[MT];
   State<D, MT> st;
 #pragma unroll
@@ -480,21 +504,8 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
       sh.q[n / (D / 32)][n % (D / 32)][lane] = query_at<D>(a, sc, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
     __syncthreads();
   }
-  Codes<D> k, v;
-  load_codes<D, false>(a, bl, 0, steps > 0, lane, k);
-  load_codes<D, true>(a, bl, 0, steps > 0, lane, v);
-  for (int n = 0; n < steps; ++n) {
-    const int j0 = (int)(j + (int64_t)n * kStep), next = (n + 1) & 31;
-    const bool more = n + 1 < steps;
-    const auto next_k = [&] { load_codes<D, false>(a, bl, next, more, lane, k); };
-    const auto next_v = [&] { load_codes<D, true>(a, bl, next, more, lane, v); };
-    const Scales s8 = scales_of(bl, n & 31);
-    if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * kStep, to, lane);
-    // hidden from somebody: the rows' positions are first .. last
-    const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && j0 <= t.last - a.window)));
-    if constexpr (MT == 1) attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, mine, g, s8, k, v, st, next_k, next_v);
-    else attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, LdsQueries<D, MT>{sh, lane}, g, s8, k, v, st, next_k, next_v);
-  }
+  if constexpr (MT == 1) walk<D, MT, CAP, FINE>(a, sc, t, j, to, kStep, steps, pos, mine, lane, st);
+  else walk<D, MT, CAP, FINE>(a, sc, t, j, to, kStep, steps, pos, LdsQueries<D>{&sh.q[0][0][0], lane}, lane, st);
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
     const float l = quad_sum(st.l[r]);
@@ -668,20 +679,84 @@ __global__ __launch_bounds__(64 * kWaves) void cache_attention_join_kernel(Cache
   if (a.lse && d == 0) a.lse[tr * a.q_heads + head] = lse_of(m, l);
 }
 
-// One workgroup a tile. Sequence i's tiles are numbered from starts[i] group /
-// R + i on; the last ones, which see most, go first.
-template <int D, int MT, bool CAP>
-__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_tiles_kernel(CacheAttend a) {
-  constexpr int R = 16 * MT;
-  __shared__ Shared<D, MT> sh;
-  const int64_t v = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
-  const int h = (int)((gridDim.x - 1 - blockIdx.x) % a.c.heads);
+// The tile that virtual tile v is, of key head h: sequence i's are numbered
+// from starts[i] group / R + i on
+template <int R>
+__device__ inline bool tile_of(const CacheAttend& a, int64_t v, int h, Tile& t) {
   const auto first = [&](int j) { return (int64_t)start_of(a.b, j) * a.group / R + j; };
   const int seq = uni(last_upto(a.b.sequences, v, first));
+  return tile_at<R>(a, seq, uni(seq_of(a.b, seq)), uni((int)(v - first(seq))), h, t);
+}
+
+// More rows: a workgroup takes a tile, its waves sharing out the tokens; the
+// last tiles, which see most, go first.
+template <int D, int MT, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_tiles_kernel(CacheAttend a) {
+  __shared__ Shared<D, MT> sh;
+  const int64_t v = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
   Tile t;
-  if (!tile_at<R>(a, seq, uni(seq_of(a.b, seq)), uni((int)(v - first(seq))), h, t)) return;
+  if (!tile_of<16 * MT>(a, v, (int)((gridDim.x - 1 - blockIdx.x) % a.c.heads), t)) return;
   const Span s = span_of(a, t.first, t.last);
   run_tile<D, MT, CAP, false>(a, t, s.from, s.to, Space{}, -1, sh);
+}
+
+// Many rows: a wave takes a tile with all its tokens, without a word to the
+// others, which have the rows beside its own, so that what one loads the
+// others find in the CU's cache. Prompts of 1501 to 6007 tokens, 64 query and
+// 8 key heads (8600 tiles): 708 us, by the kernel above 811; one of 4096, 32
+// heads each with its own keys (2080 tiles, a single round here): 190 and 175.
+template <int D, int MT, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_rows_kernel(CacheAttend a) {
+  constexpr int R = 16 * MT, W = D / 16;
+  __shared__ ca_u32x4 queries[kWaves][MT * (D / 32) * 64];
+  const int lane = threadIdx.x & 63, wave = uni((int)(threadIdx.x >> 6));
+  const int lo16 = lane & 15, g = lane >> 4;
+  const int64_t v = (int64_t)((gridDim.x - 1 - blockIdx.x) / a.c.heads) * kWaves + wave;
+  const int h = (int)((gridDim.x - 1 - blockIdx.x) % a.c.heads);
+  Tile t;
+  if (!tile_of<R>(a, v, h, t)) return;
+  const Scores sc = scores_of(a, CAP);
+  const Span s = span_of(a, t.first, t.last);
+  const int64_t from = uni(s.from), to = uni(s.to);
+  const int rows = t.s.n * a.group;
+#pragma unroll
+  for (int n = 0; n < MT * (D / 32); ++n)
+    queries[wave][n * 64 + lane] = query_at<D>(a, sc, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
+  int pos[MT];
+  State<D, MT> st;
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    const int row = t.r0 + 16 * r + lo16;
+    pos[r] = row < rows ? (int)t.s.p0 + row / a.group : -1;
+    st.m[r] = -__builtin_inff();
+    st.l[r] = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) st.o[r][i] = (bq_f32x4){0, 0, 0, 0};
+  }
+  // the wave's own lanes read them: LDS serves a wave in order
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  walk<D, MT, CAP, false>(a, sc, t, from, to, kGroup, (int)((to - from + kGroup - 1) / kGroup), pos,
+                          LdsQueries<D>{queries[wave], lane}, lane, st);
+  int lane_ = lane;
+  asm volatile("" : "+v"(lane_));  // computed here, and not held in registers through the loop
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    const float sum = quad_sum(st.l[r]), inv = sum == 0 ? 0.0f : 1.0f / sum;
+    const int row = t.r0 + 16 * r + (lane_ & 15);
+    if (row >= rows) continue;
+    const int head = t.h * a.group + row % a.group;
+    const int64_t tr = t.s.row0 + row / a.group;
+    uint16_t* out = a.out.p + tr * a.out.tok + head * a.out.head + 4 * W * (lane_ >> 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *(bq_u32x2_a2*)(out + W * k + i) = (bq_u32x2){pack_bf16(st.o[r][i][k] * inv, st.o[r][i + 1][k] * inv),
+                                                      pack_bf16(st.o[r][i + 2][k] * inv, st.o[r][i + 3][k] * inv)};
+    if (a.lse && lane_ < 16) a.lse[tr * a.q_heads + head] = lse_of(st.m[r], sum);
+  }
 }
 
 // Rows of a tile and whether a workgroup takes whole tiles: by the mean rows
@@ -704,6 +779,8 @@ Form form_of(const CacheAttend& a, int head_dim) {
   f.tiles = a.b.starts && f.mt > 1 && rows > 32 && f.count >= 2 * kShares;
   return f;
 }
+constexpr int64_t kRowsTiles = 5 * kShares;  // of waves that take whole tiles: more than a round of them
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 Space space_of(void* ws, int mt, int head_dim, size_t* bytes) {
   const size_t rows = (size_t)2 * kShares * 16 * mt;
@@ -717,6 +794,12 @@ template <int D, int MT>
 hipError_t run(const CacheAttend& a, const Form& f, const Space& ws, hipStream_t st) {
   const dim3 block(64 * kWaves);
   if constexpr (MT > 1) {
+    if (f.tiles && f.count >= kRowsTiles) {
+      const unsigned grid = (unsigned)((f.count / a.c.heads + kWaves - 1) / kWaves * a.c.heads);
+      if (a.cap > 0) cache_attention_rows_kernel<D, MT, true><<<grid, block, 0, st>>>(a);
+      else cache_attention_rows_kernel<D, MT, false><<<grid, block, 0, st>>>(a);
+      return hipGetLastError();
+    }
     if (f.tiles) {
       if (a.cap > 0) cache_attention_tiles_kernel<D, MT, true><<<(unsigned)f.count, block, 0, st>>>(a);
       else cache_attention_tiles_kernel<D, MT, false><<<(unsigned)f.count, block, 0, st>>>(a);
