@@ -112,15 +112,24 @@ fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, 
  * heads) of the cache.
  *   s = scale q . k;  if softcap > 0: s = softcap tanh(s / softcap);
  *   out = sum over the seen of softmax(s) v,  lse = log(sum of exp(s)).
- * Where nothing is seen, or only scores of -inf, out is 0 and lse -inf. Keys and values enter the
- * products exactly, weights rounded to bf16 (scaled by up to 2^8); sums and
- * the softmax are 32-bit, out is bf16 (any strides), lse fp32 [tokens,
- * q_heads] or NULL. A NaN in a key or value reaches the queries that see it
- * and no others.
+ * Where nothing is seen, or only scores of -inf, out is 0 and lse -inf. Keys
+ * and values enter the products exactly, sums and the softmax are 32-bit, out
+ * is bf16 (any strides), lse fp32 [tokens, q_heads] or NULL. Weights enter as
+ * two bf16 each, 2^-17 off, so that out is as far off as its own rounding;
+ * of prompts large enough to wait for the products and not for memory
+ * (FP8_CACHE_TILES and _ROWS) as one, 2^-9 off. A NaN in a key or value
+ * reaches the queries that see it and no others.
  *   ws: fp8_cache_attention_workspace_bytes of the same cache and batch
  *   (their sizes alone count), 16-B aligned; it holds nothing between calls.
  */
 size_t fp8_cache_attention_workspace_bytes(const fp8_cache* cache, const fp8_cache_batch* batch, int q_heads);
+/* The rows (queries of one key head) that are computed together, and how the
+ * work is cut, by the sizes alone. For profiles and tests; 0 and 0 of an empty
+ * batch. */
+#define FP8_CACHE_SHARES 0 /* equal shares of all tokens a workgroup */
+#define FP8_CACHE_TILES 1  /* a tile of rows a workgroup */
+#define FP8_CACHE_ROWS 2   /* a tile of rows a wave */
+fp8_status fp8_cache_attention_plan(const fp8_cache* cache, const fp8_cache_batch* batch, int q_heads, int* rows, int* form);
 fp8_status fp8_cache_attention(const fp8_cache* cache, const fp8_cache_batch* batch, const fp8_cache_rows* q, int q_heads,
                                float scale, float softcap, int window, const fp8_cache_rows* out, float* lse, void* ws,
                                size_t ws_bytes, hipStream_t stream);

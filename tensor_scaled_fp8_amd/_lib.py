@@ -82,6 +82,7 @@ SIGNATURES = {
     "fp8_cache_append": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_vp, c_int, c_int, c_vp]),
     "fp8_cache_read": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp]),
     "fp8_cache_attention_workspace_bytes": (c_sz, [c_vp, c_vp, c_int]),
+    "fp8_cache_attention_plan": (c_int, [c_vp, c_vp, c_int, c_intp, c_intp]),
     "fp8_cache_attention": (c_int, [c_vp, c_vp, c_vp, c_int, ctypes.c_float, ctypes.c_float, c_int, c_vp, c_vp, c_vp,
                                     c_sz, c_vp]),
     "fp4_codes_bytes": (c_sz, [c_i64, c_i64]),

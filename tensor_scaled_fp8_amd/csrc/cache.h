@@ -98,6 +98,7 @@ struct CacheAttend {
   int window;
 };
 size_t cache_attention_ws_bytes(const CacheAttend& a, int head_dim);
+void cache_attention_plan(const CacheAttend& a, int head_dim, int* rows, int* form);
 hipError_t launch_cache_attention(const CacheAttend& a, int head_dim, void* ws, hipStream_t st);
 
 }  // namespace fp8lin

@@ -254,19 +254,22 @@ inline int part_cols(int64_t N, int most) {
   return (int)((N + 256 * c - 1) / (256 * c));
 }
 
-// Of more rows: a workgroup's tile is 16 MF rows by 64 NB columns. Its four
-// waves have 16 NB columns each, whose codes go from memory to registers in
-// the instruction's order; X's tile goes over LDS, a block of 128 of K at a
-// time in turn with the one before. The scaled instruction takes 4-bit and
-// 8-bit codes as they are.
+// Of more rows: a workgroup's tile is 16 MF rows by 64 NB columns. Four waves
+// have 16 NB columns each, whose codes go from memory to registers in the
+// instruction's order; X's tile goes over LDS, a block of 128 of K at a time
+// in turn with the one before. The scaled instruction takes 4-bit and 8-bit
+// codes as they are. KG groups of four waves take every KG-th block of K each
+// and add their sums at the end: where a CU has no other workgroup, its SIMDs
+// then have two waves (222 rows by 7040 x 1664, 104 workgroups: 19.1 us with
+// one group, 14.0 with two; 512 by 12288 x 16384, 512 of them: 96 and 113).
 typedef int f4_v8i __attribute__((ext_vector_type(8)));
 
-template <int MF, int NB>
-__global__ __launch_bounds__(256) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_t* __restrict__ y, int tiles_n) {
+template <int MF, int NB, int KG>
+__global__ __launch_bounds__(256 * KG) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_t* __restrict__ y, int tiles_n) {
   constexpr int kPieces = 2 * MF, kTurns = (kPieces + 3) / 4;  // of 1024 bytes; each wave's
-  __shared__ bq_u32x4 xl[2][kPieces][64];
+  __shared__ bq_u32x4 xl[KG][2][kPieces][64];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all & 3, kg = all >> 2;
   const int r16 = lane & 15, G = lane >> 4;
   const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * MF;  // in 16 rows
   const int64_t p0 = ((int64_t)(blockIdx.x % tiles_n) * 4 + wave) * NB;
@@ -296,56 +299,108 @@ __global__ __launch_bounds__(256) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_
   for (int f = 0; f < MF; ++f)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[f][b] = (bq_f32x4){0, 0, 0, 0};
-  bq_u32x4 xv[kTurns], wv[4][NB];
-  uint32_t wsv[NB], xsv[MF];
-  const auto load_x = [&](int kb) {
-    const int k = kb < nk ? kb : nk - 1;
+  // step n of this group is block n KG + kg of K; loads past the last repeat it
+  bq_u32x4 xv[2][kTurns], wv[4][NB];
+  uint32_t wsv[NB], xsv[MF], wsn[NB], xsn[MF];  // scales of four blocks of K, and of the next four
+  const auto load_x = [&](int n, bq_u32x4 (&v)[kTurns]) {
+    const int k = n * KG + kg < nk ? n * KG + kg : nk - 1;
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) xv[i] = *(const bq_u32x4*)(xc[i] + (int64_t)k * 2048);
+    for (int i = 0; i < kTurns; ++i) v[i] = *(const bq_u32x4*)(xc[i] + (int64_t)k * 2048);
   };
-  const auto store_x = [&](int buf) {
+  const auto store_x = [&](int buf, const bq_u32x4 (&v)[kTurns]) {
 #pragma unroll
     for (int i = 0; i < kTurns; ++i)
-      if (wave + 4 * i < kPieces) xl[buf][wave + 4 * i][lane] = xv[i];
+      if (wave + 4 * i < kPieces) xl[kg][buf][wave + 4 * i][lane] = v[i];
   };
-  const auto load_w = [&](int kb, bq_u32x4 (&v)[NB]) {
-    const int k = kb < nk ? kb : nk - 1;
+  const auto load_w = [&](int n, bq_u32x4 (&v)[NB]) {
+    const int k = n * KG + kg < nk ? n * KG + kg : nk - 1;
 #pragma unroll
     for (int b = 0; b < NB; ++b) v[b] = *(const bq_u32x4*)(wc[b] + (int64_t)k * 1024);
   };
-  load_x(0);
+  const auto load_scales = [&](int k4) {
+    const int64_t at = k4 < xk4 ? k4 : xk4 - 1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wsn[b] = *(const uint32_t*)(ws[b] + at * 256);
+#pragma unroll
+    for (int f = 0; f < MF; ++f) xsn[f] = *(const uint32_t*)(xs[f] + at * 64);
+  };
+  load_scales(0);
+  load_x(0, xv[0]);
   load_w(0, wv[0]);
+  load_x(1, xv[1]);
   load_w(1, wv[1]);
   load_w(2, wv[2]);
-  store_x(0);
-  load_x(1);
+  store_x(0, xv[0]);
+  load_x(2, xv[0]);
   lds_barrier();
-  for (int k4 = 0; k4 < nk; k4 += 4) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b) wsv[b] = *(const uint32_t*)(ws[b] + (int64_t)(k4 >> 2) * 256);
-#pragma unroll
-    for (int f = 0; f < MF; ++f) xsv[f] = *(const uint32_t*)(xs[f] + (int64_t)(k4 >> 2) * 64);
+  const int steps = (nk + KG - 1) / KG;
+  for (int n4 = 0; n4 < steps; n4 += 4) {
     static_for<4>([&](auto I_) {
       constexpr int i = decltype(I_)::value;
-      const int kb = k4 + i;
-      if (kb < nk) {
-        load_w(kb + 3, wv[(i + 3) & 3]);
-        static_for<MF>([&](auto F_) {
-          constexpr int f = decltype(F_)::value;
-          const bq_u32x4 p = xl[i & 1][2 * f][lane], q = xl[i & 1][2 * f + 1][lane];
-          const f4_v8i e = {(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
-          static_for<NB>([&](auto B_) {
-            constexpr int b = decltype(B_)::value;
-            const bq_u32x4 c = wv[i][b];
-            const f4_v8i a = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
-            acc[f][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, e, acc[f][b], 4, 0, i, (int)wsv[b], i, (int)xsv[f]);
+      const int n = n4 + i, kb = n * KG + kg;
+      if (n < steps) {
+        if constexpr (i * KG % 4 == 0) {
+          // this group's first block lowest
+#pragma unroll
+          for (int b = 0; b < NB; ++b) wsv[b] = wsn[b] >> (8 * kg);
+#pragma unroll
+          for (int f = 0; f < MF; ++f) xsv[f] = xsn[f] >> (8 * kg);
+          load_scales(kb / 4 + 1);
+        }
+        constexpr int sel = i * KG % 4;
+        load_w(n + 3, wv[(i + 3) & 3]);
+        if (kb < nk) {
+          // a fragment is read while the one before is multiplied
+          bq_u32x4 p[2], q[2];
+          p[0] = xl[kg][i & 1][0][lane];
+          q[0] = xl[kg][i & 1][1][lane];
+          static_for<MF>([&](auto F_) {
+            constexpr int f = decltype(F_)::value, at = f & 1;
+            if constexpr (f + 1 < MF) {
+              p[at ^ 1] = xl[kg][i & 1][2 * f + 2][lane];
+              q[at ^ 1] = xl[kg][i & 1][2 * f + 3][lane];
+            }
+            const f4_v8i e = {(int)p[at].x, (int)p[at].y, (int)p[at].z, (int)p[at].w,
+                              (int)q[at].x, (int)q[at].y, (int)q[at].z, (int)q[at].w};
+            static_for<NB>([&](auto B_) {
+              constexpr int b = decltype(B_)::value;
+              const bq_u32x4 c = wv[i][b];
+              const f4_v8i a = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+              acc[f][b] =
+                  __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, e, acc[f][b], 4, 0, sel, (int)wsv[b], sel, (int)xsv[f]);
+            });
+            __builtin_amdgcn_sched_barrier(0);
           });
-        });
-        store_x((i + 1) & 1);
-        load_x(kb + 2);
+        }
+        store_x((i + 1) & 1, xv[(i + 1) & 1]);
+        load_x(n + 3, xv[(i + 1) & 1]);
         lds_barrier();
       }
     });
+  }
+  if constexpr (KG > 1) {
+    // the second group's sums over LDS, as many fragments at a time as fit
+    static_assert(KG == 2, "two groups are joined");
+    constexpr int kAtOnce = KG * 2 * kPieces / (4 * NB) < MF ? KG * 2 * kPieces / (4 * NB) : MF;
+    bq_f32x4* const part = (bq_f32x4*)&xl[0][0][0][0];
+#pragma unroll
+    for (int f0 = 0; f0 < MF; f0 += kAtOnce) {
+      if (f0) lds_barrier();
+      if (kg == 1) {
+#pragma unroll
+        for (int f = f0; f < MF && f < f0 + kAtOnce; ++f)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) part[(((f - f0) * 4 + wave) * NB + b) * 64 + lane] = acc[f][b];
+      }
+      lds_barrier();
+      if (kg == 0) {
+#pragma unroll
+        for (int f = f0; f < MF && f < f0 + kAtOnce; ++f)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[f][b] += part[(((f - f0) * 4 + wave) * NB + b) * 64 + lane];
+      }
+    }
+    if (kg) return;
   }
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
@@ -366,7 +421,9 @@ __global__ __launch_bounds__(256) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_
 template <int MF, int NB>
 hipError_t run_many(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
   const int64_t tm = ((x.M + 15) / 16 + MF - 1) / MF, tn = (w.N + 64 * NB - 1) / (64 * NB);
-  fp4_many_kernel<MF, NB><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
+  // two groups where a CU has one workgroup at most; else two workgroups share it
+  if (tm * tn <= 256) fp4_many_kernel<MF, NB, 2><<<(unsigned)(tm * tn), 512, 0, st>>>(x, w, y, (int)tn);
+  else fp4_many_kernel<MF, NB, 1><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
   return hipGetLastError();
 }
 template <int MF>

@@ -118,6 +118,15 @@ size_t fp8_cache_attention_workspace_bytes(const fp8_cache* cache, const fp8_cac
   return cache_attention_ws_bytes(attend_of(cache, batch, q_heads), cache->head_dim);
 }
 
+fp8_status fp8_cache_attention_plan(const fp8_cache* cache, const fp8_cache_batch* batch, int q_heads, int* rows, int* form) {
+  if (!cache || !cache_sizes(cache->pages, cache->page_tokens, cache->heads, cache->head_dim) || !batch ||
+      batch->tokens < 0 || batch->sequences < 0 || !q_heads_ok(q_heads, cache->heads) || !rows || !form)
+    return FP8_ERR_INVALID;
+  if (!attend_fits(batch, q_heads)) return FP8_ERR_UNSUPPORTED;
+  cache_attention_plan(attend_of(cache, batch, q_heads), cache->head_dim, rows, form);
+  return FP8_OK;
+}
+
 fp8_status fp8_cache_attention(const fp8_cache* cache, const fp8_cache_batch* batch, const fp8_cache_rows* q, int q_heads,
                                float scale, float softcap, int window, const fp8_cache_rows* out, float* lse, void* ws,
                                size_t ws_bytes, hipStream_t stream) {

@@ -19,7 +19,7 @@ BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
 def test_header_functions_all_exported():
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "fp8lin_serve.h")).read(), flags=re.S)
     names = set(re.findall(r"^\s*[A-Za-z_][\w\s\*]*?\b(fp[48]_\w+)\s*\(", src, flags=re.M))
-    assert len(names) == 12
+    assert len(names) == 13
     lib = tsf.load()
     for n in names:
         assert hasattr(lib, n) and n in _lib.SIGNATURES, n
@@ -100,6 +100,32 @@ def test_sizes():
     assert lib.fp4_codes_bytes(513, 17) == 4 * 4096 and lib.fp4_codes_bytes(0, 5) == lib.fp4_codes_bytes(-1, 5) == 0
 
 
+def plan(tokens, sequences, q_heads, heads, d, starts=True, table_pages=64):
+    rows, form = ctypes.c_int(), ctypes.c_int()
+    c, b = Cache(**{**CACHE, "heads": heads, "head_dim": d}), Batch(**{**BATCH, "tokens": tokens, "sequences": sequences,
+                                                                      "starts": OK if starts else None, "table_pages": table_pages})
+    assert tsf.load().fp8_cache_attention_plan(ctypes.byref(c), ctypes.byref(b), q_heads, ctypes.byref(rows),
+                                               ctypes.byref(form)) == 0
+    return rows.value, form.value
+
+
+def test_attention_forms():
+    """The sizes that the GPU tests take reach every form."""
+    from tests.test_gpu_cache_attention_forms import CASES, SHARES, TILES, ROWS
+    seen = {}
+    for form, heads, hq, d, lens, new in CASES:
+        got = plan(sum(new), len(new), hq, heads, d)
+        assert got[1] == form, (heads, hq, d, got)
+        seen.setdefault(form, set()).add((d, got[0]))
+    wide = {(64, 64), (128, 64), (256, 32)}
+    assert seen[TILES] == seen[ROWS] == wide and seen[SHARES] == wide | {(64, 32), (128, 32), (64, 16), (128, 16), (256, 16)}
+    assert plan(0, 3, 4, 2, 64) == (0, 0) and plan(5, 5, 4, 2, 64, starts=False) == (16, SHARES)
+    lib, r = tsf.load(), ctypes.c_int()
+    assert lib.fp8_cache_attention_plan(None, None, 4, ctypes.byref(r), ctypes.byref(r)) == INV
+    bad = Batch(**{**BATCH, "starts": OK, "tokens": 1 << 40})
+    assert lib.fp8_cache_attention_plan(ctypes.byref(Cache(**CACHE)), ctypes.byref(bad), 4, ctypes.byref(r), ctypes.byref(r)) == UNS
+
+
 def test_fp4_arguments_without_launch():
     lib = tsf.load()
     q, d, f = lib.fp4_quantize, lib.fp4_dequantize, lib.fp4_linear_fwd_cached
@@ -110,7 +136,7 @@ def test_fp4_arguments_without_launch():
             assert g(*args(**change), None) == INV, change
         assert g(*args(K=(1 << 20) + 1), None) == UNS
     assert d(OK, OK, 32, 16, OK, 8, None) == INV
-    ok = dict(X=OK, ldx=32, M=4, K=32, N=16, c=OK, s=OK, ws=OK, n=1 << 30, Y=OK)
+    ok = dict(X=OK, ldx=32, M=20, K=32, N=16, c=OK, s=OK, ws=OK, n=1 << 30, Y=OK)
     for change in (dict(X=None), dict(X=OK + 1), dict(M=-1), dict(ldx=-1), dict(c=None), dict(s=OK + 8), dict(ws=None),
                    dict(ws=OK + 8), dict(n=0), dict(Y=None)):
         assert f(*{**ok, **change}.values(), None) == INV, change
