@@ -42,6 +42,12 @@ hipError_t launch_fp4_x(const Bf16Mat& x, const Fp4X& q, hipStream_t st);
 // instructions FEW_64_8); of more, of the 8-bit and 4-bit codes.
 constexpr int64_t kFp4Few = 64;
 bool fp4_fused(int64_t M, int64_t K);
+struct Fp4Form {
+  int kind;             // FP4_FUSED, _FEW or _MANY
+  int mf, nb, groups;   // 16-row fragments of X and 16-column ones of W a wave, groups of waves over K
+  int cols;             // of Y a workgroup (fused, few)
+};
+Fp4Form fp4_form(int64_t M, int64_t K, int64_t N);
 hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
 hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
 

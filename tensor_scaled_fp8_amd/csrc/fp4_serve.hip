@@ -419,16 +419,18 @@ __global__ __launch_bounds__(256 * KG) void fp4_many_kernel(Fp4X x, Fp4Mat w, ui
 }
 
 template <int MF, int NB>
-hipError_t run_many(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
+hipError_t run_many(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* y, hipStream_t st) {
   const int64_t tm = ((x.M + 15) / 16 + MF - 1) / MF, tn = (w.N + 64 * NB - 1) / (64 * NB);
-  // two groups where a CU has one workgroup at most; else two workgroups share it
-  if (tm * tn <= 256) fp4_many_kernel<MF, NB, 2><<<(unsigned)(tm * tn), 512, 0, st>>>(x, w, y, (int)tn);
-  else fp4_many_kernel<MF, NB, 1><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
+  // (one fragment of columns never goes with more workgroups than CUs: two would take one round less)
+  if (NB == 1 || f.groups == 2) fp4_many_kernel<MF, NB, 2><<<(unsigned)(tm * tn), 512, 0, st>>>(x, w, y, (int)tn);
+  else if constexpr (NB > 1) fp4_many_kernel<MF, NB, 1><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
   return hipGetLastError();
 }
 template <int MF>
-hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, int nb, uint16_t* y, hipStream_t st) {
-  return nb == 1 ? run_many<MF, 1>(x, w, y, st) : nb == 2 ? run_many<MF, 2>(x, w, y, st) : run_many<MF, 3>(x, w, y, st);
+hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* y, hipStream_t st) {
+  if constexpr (MF < 8)
+    if (f.nb == 1) return run_many<MF, 1>(x, w, f, y, st);
+  return f.nb == 2 ? run_many<MF, 2>(x, w, f, y, st) : run_many<MF, 3>(x, w, f, y, st);
 }
 
 }  // namespace
@@ -436,42 +438,58 @@ hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, int nb, uint16_t* y, hipStre
 // X's values in bf16 fit 64 KB of LDS
 bool fp4_fused(int64_t M, int64_t K) { return M <= 16 && M * fp4_xblocks(K) <= 248; }
 
+Fp4Form fp4_form(int64_t M, int64_t K, int64_t N) {
+  Fp4Form f = {fp4_fused(M, K) ? FP4_FUSED : M <= kFp4Few ? FP4_FEW : FP4_MANY, 1, 1, 1, 0};
+  if (f.kind != FP4_MANY) {
+    f.mf = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    f.cols = part_cols(N, 48);
+    f.nb = f.cols <= 16 ? 1 : f.cols <= 32 ? 2 : 3;
+    return f;
+  }
+  // the tile whose rounds of 256 workgroups have the least products in all
+  const int64_t mt = (M + 15) / 16, panels = (N + 15) / 16;
+  int64_t least = 0;
+  for (int mf = 4; mf <= 8; ++mf)
+    for (int nb = mf == 8 ? 2 : 1; nb <= 3; ++nb) {  // 8 x 1 costs what 4 x 2 does
+      const int64_t n = (mt + mf - 1) / mf * ((panels + 4 * nb - 1) / (4 * nb));
+      // 4 + products: what a block of K costs a wave besides them
+      const int64_t cost = (n + 255) / 256 * (mf * nb + 4);
+      if (least == 0 || cost < least) {
+        least = cost;
+        f.mf = mf;
+        f.nb = nb;
+        // two groups where a CU has one workgroup at most; else two workgroups share it
+        f.groups = n <= 256 ? 2 : 1;
+      }
+    }
+  return f;
+}
+
 hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
   if (x.rows == 0 || w.N == 0) return hipSuccess;
   const Fp4X none = {nullptr, nullptr, 0, 0};
-  const int cols = part_cols(w.N, 48);
-  return cols <= 16   ? run<true, 1, 1, 4>(x, none, w, y, cols, st)
-         : cols <= 32 ? run<true, 1, 2, 4>(x, none, w, y, cols, st)
-                      : run<true, 1, 3, 4>(x, none, w, y, cols, st);
+  const Fp4Form f = fp4_form(x.rows, w.K, w.N);
+  return f.nb == 1   ? run<true, 1, 1, 4>(x, none, w, y, f.cols, st)
+         : f.nb == 2 ? run<true, 1, 2, 4>(x, none, w, y, f.cols, st)
+                     : run<true, 1, 3, 4>(x, none, w, y, f.cols, st);
 }
 
 hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
   if (x.M == 0 || w.N == 0) return hipSuccess;
-  if (x.M <= kFp4Few) {
+  const Fp4Form f = fp4_form(x.M, w.K, w.N);
+  if (f.kind != FP4_MANY) {
     const Bf16Mat none = {nullptr, 0, 0, 0};
-    const int cols = part_cols(w.N, 48), mf = x.M <= 16 ? 1 : x.M <= 32 ? 2 : 4, nb = cols <= 16 ? 1 : cols <= 32 ? 2 : 3;
 #define FEW(m, n) \
-  if (mf == m && nb == n) return run<false, m, n, (m > 2 ? 2 : 4)>(none, x, w, y, cols, st);
+  if (f.mf == m && f.nb == n) return run<false, m, n, (m > 2 ? 2 : 4)>(none, x, w, y, f.cols, st);
     FEW(1, 1) FEW(1, 2) FEW(1, 3) FEW(2, 1) FEW(2, 2) FEW(2, 3) FEW(4, 1) FEW(4, 2) FEW(4, 3)
 #undef FEW
   }
-  // the tile whose rounds of 256 workgroups have the least products in all
-  const int64_t mt = (x.M + 15) / 16, panels = (w.N + 15) / 16;
-  int best_mf = 4, best_nb = 1;
-  double least = 0;
-  for (int mf = 4; mf <= 8; ++mf)
-    for (int nb = 1; nb <= 3; ++nb) {
-      const int64_t groups = (mt + mf - 1) / mf * ((panels + 4 * nb - 1) / (4 * nb));
-      // 4 + products: what a block of K costs a wave besides them
-      const double cost = (double)((groups + 255) / 256) * (mf * nb + 4);
-      if (least == 0 || cost < least) least = cost, best_mf = mf, best_nb = nb;
-    }
-  switch (best_mf) {
-    case 4: return run_rows<4>(x, w, best_nb, y, st);
-    case 5: return run_rows<5>(x, w, best_nb, y, st);
-    case 6: return run_rows<6>(x, w, best_nb, y, st);
-    case 7: return run_rows<7>(x, w, best_nb, y, st);
-    default: return run_rows<8>(x, w, best_nb, y, st);
+  switch (f.mf) {
+    case 4: return run_rows<4>(x, w, f, y, st);
+    case 5: return run_rows<5>(x, w, f, y, st);
+    case 6: return run_rows<6>(x, w, f, y, st);
+    case 7: return run_rows<7>(x, w, f, y, st);
+    default: return run_rows<8>(x, w, f, y, st);
   }
 }
 

@@ -153,31 +153,28 @@ def tolerance(out, mass, size, d):
 GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
 
 
+MIDDLES = (GRID[1:] + GRID[:-1]) / 2
+
+
 def fp4_codes(w):
-    """codes (0 .. 15) and biases of w [K, N], groups of 32 along K; a group with a NaN has bias None (as nan)."""
+    """codes (0 .. 15) and biases of w [K, N], groups of 32 along K; a group with a NaN has bias nan."""
     w = np.asarray(w, dtype=np.float64)
     K, N = w.shape
     g = -(-K // 32)
     p = np.zeros((g * 32, N))
     p[:K] = w
     p = p.reshape(g, 32, N)
-    codes, bias = np.zeros(p.shape, dtype=np.uint8), np.zeros((g, N))
-    for i in range(g):
-        for n in range(N):
-            x = p[i, :, n]
-            if np.isnan(x).any():
-                bias[i, n] = np.nan
-                continue
-            a = np.abs(x).max()
-            b = 0 if a == 0 or np.isinf(a) else bias_of(a, 6.0)
-            bias[i, n] = b
-            y = np.minimum(np.abs(x) * 2.0 ** b, 6.0)
-            dist = np.abs(y[:, None] - GRID)
-            near = dist.min(1, keepdims=True) == dist
-            # of two equally near ones, the even code
-            pick = np.where(near.sum(1) == 2, np.argmax(near & (np.arange(8) % 2 == 0), 1), np.argmax(near, 1))
-            codes[i, :, n] = pick | (np.signbit(x).astype(np.uint8) << 3)
-    return codes, bias
+    with np.errstate(invalid="ignore"):
+        a = np.abs(p).max(1)
+    ok = np.isfinite(a) & (a > 0)
+    m, e = np.frexp(np.where(ok, a, 1.0))
+    b = np.where(ok, np.clip(3 - e - (m > 0.75), -126, 126), 0)           # 6 = 0.75 2^3
+    assert ((a * 2.0 ** b <= 6) | ~ok | (b == -126)).all() and ((a * 2.0 ** (b + 1) > 6) | ~ok | (b == 126)).all()
+    y = np.minimum(np.abs(p) * 2.0 ** b[:, None], 6.0)
+    codes = np.zeros(p.shape, dtype=np.uint8)
+    for i, mid in enumerate(MIDDLES):
+        codes += (y >= mid) if i % 2 else (y > mid)                       # a middle goes to the even code
+    return codes | (np.signbit(p).astype(np.uint8) << 3), np.where(np.isnan(a), np.nan, b)
 
 
 def fp4_held(w):

@@ -57,8 +57,31 @@ def test_borders_and_extremes():
     assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 
+def stored8(x):
+    """held, by rows of many blocks at once."""
+    x = np.asarray(x)
+    if not np.isfinite(x).all():
+        return held(x)
+    m, k = x.shape
+    p = np.zeros((m, -(-k // 128) * 128))
+    p[:, :k] = x
+    p = p.reshape(m, -1, 128)
+    a = np.abs(p).max(2, keepdims=True)
+    f, e = np.frexp(np.where(a > 0, a, 1.0))
+    b = np.where(a > 0, np.clip(9 - e - (f > 0.875), -126, 126), 0)       # 448 = 0.875 2^9
+    y = p * 2.0 ** b
+    gap = 2.0 ** (np.maximum(np.frexp(np.where(y == 0, 1.0, y))[1] - 1, -6) - 3)
+    return (np.round(y / gap) * gap * 2.0 ** -b).reshape(m, -1)[:, :k]
+
+
+def test_stored8_is_held():
+    g = np.random.Generator(np.random.PCG64(1))
+    x = to_bf16(g.standard_normal((9, 300)) * np.exp2(g.integers(-9, 9, size=(9, 300))))
+    assert np.array_equal(stored8(x), held(x))
+
+
 def check(x, w, y):
-    a, b = held(x), fp4_held(w)
+    a, b = stored8(x), fp4_held(w)
     want = a @ b
     got = host(y)
     assert got.shape == want.shape
@@ -82,6 +105,36 @@ def test_linear(M, K, N):
     out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
     assert tsf.fp4_linear_fwd_cached(wide[:, 1:K + 1], q, out) is out
     assert torch.equal(out, y)                                             # any pitch, the same bits
+
+
+# (form, row tiles, column tiles, groups over K) and rows and columns that choose them
+FORMS = {
+    (0, 1, 1, 1): (3, 70), (0, 1, 2, 1): (1, 4120), (0, 1, 3, 1): (2, 8200),
+    (1, 1, 1, 1): (16, 90), (1, 1, 2, 1): (16, 4120), (1, 1, 3, 1): (15, 8200), (1, 2, 1, 1): (21, 16), (1, 2, 2, 1): (32, 4120),
+    (1, 2, 3, 1): (21, 8200), (1, 4, 1, 1): (36, 50), (1, 4, 2, 1): (64, 4120), (1, 4, 3, 1): (50, 8200),
+    (2, 4, 1, 2): (65, 16), (2, 5, 1, 2): (65, 8200), (2, 6, 1, 2): (83, 8200), (2, 7, 1, 2): (101, 8200),
+    (2, 4, 2, 2): (113, 8200), (2, 5, 2, 2): (65, 16600), (2, 6, 2, 2): (257, 9880), (2, 7, 2, 2): (197, 12520),
+    (2, 8, 2, 2): (245, 12520), (2, 4, 3, 2): (83, 16600), (2, 5, 3, 2): (131, 16600), (2, 6, 3, 2): (161, 16600),
+    (2, 7, 3, 2): (197, 16600), (2, 8, 3, 2): (245, 16600), (2, 4, 2, 1): (293, 12520), (2, 5, 2, 1): (227, 16600),
+    (2, 6, 2, 1): (257, 19720), (2, 7, 2, 1): (323, 16600), (2, 8, 2, 1): (341, 19720), (2, 4, 3, 1): (257, 16600),
+    (2, 5, 3, 1): (341, 16600), (2, 6, 3, 1): (401, 16600), (2, 7, 3, 1): (600, 14680), (2, 8, 3, 1): (500, 19720)}
+
+
+def blocks_of(form):
+    """K: from one block of 128 to ten, ends within one; above 16 blocks a row, so that few rows are not fused."""
+    if form[0] == 1:
+        return 2000 + 37 * sum(form)
+    return (90, 200, 385, 640, 777, 1200)[(form[1] + form[2] + form[3]) % 6]
+
+
+@pytest.mark.parametrize("form", list(FORMS), ids=str)
+def test_every_form(form):
+    M, N = FORMS[form]
+    K = blocks_of(form)
+    g = np.random.Generator(np.random.PCG64(M + N))
+    x = to_bf16(g.standard_normal((M, K)) * np.exp2(g.integers(-6, 6, size=(M, 1))))
+    w = weight(g, K, N)
+    check(x, w, tsf.fp4_linear_fwd_cached(up(x), tsf.prepare_fp4_weight(up(w))))
 
 
 @pytest.mark.parametrize("M", [1, 20, 200])

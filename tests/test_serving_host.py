@@ -19,7 +19,7 @@ BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
 def test_header_functions_all_exported():
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "fp8lin_serve.h")).read(), flags=re.S)
     names = set(re.findall(r"^\s*[A-Za-z_][\w\s\*]*?\b(fp[48]_\w+)\s*\(", src, flags=re.M))
-    assert len(names) == 13
+    assert len(names) == 14
     lib = tsf.load()
     for n in names:
         assert hasattr(lib, n) and n in _lib.SIGNATURES, n
@@ -124,6 +124,24 @@ def test_attention_forms():
     assert lib.fp8_cache_attention_plan(None, None, 4, ctypes.byref(r), ctypes.byref(r)) == INV
     bad = Batch(**{**BATCH, "starts": OK, "tokens": 1 << 40})
     assert lib.fp8_cache_attention_plan(ctypes.byref(Cache(**CACHE)), ctypes.byref(bad), 4, ctypes.byref(r), ctypes.byref(r)) == UNS
+
+
+def test_fp4_forms():
+    """The sizes that the GPU tests take reach every form that any size up to 700 rows chooses."""
+    from tests.test_gpu_fp4 import FORMS, blocks_of
+
+    def fp4_plan(M, K, N):
+        v = [ctypes.c_int() for _ in range(4)]
+        assert tsf.load().fp4_linear_plan(M, K, N, *map(ctypes.byref, v)) == 0
+        return tuple(x.value for x in v)
+    for form, (M, N) in FORMS.items():
+        assert fp4_plan(M, blocks_of(form), N) == form
+    seen = {fp4_plan(M, K, N) for M in (1, 2, 16, 17, 32, 33, 64, *range(65, 700, 13)) for K in (200, 4000)
+            for N in (1, 17, 300, 4096, 4097, 8193, *range(9000, 40000, 700))}
+    assert seen <= set(FORMS), seen - set(FORMS)
+    assert tsf.load().fp4_linear_plan(-1, 1, 1, *[ctypes.byref(ctypes.c_int())] * 4) == INV
+    assert tsf.load().fp4_linear_plan(1 << 40, 1, 1, *[ctypes.byref(ctypes.c_int())] * 4) == UNS
+    assert tsf.load().fp4_linear_plan(1, 1, 1, None, None, None, None) == INV
 
 
 def test_fp4_arguments_without_launch():
