@@ -90,7 +90,9 @@ size_t fp8_cache_scales_bytes(int64_t pages, int page_tokens, int heads, int hea
  *          are 0; at most 0 if one is infinite;
  *   bias = need if the block's first token is among them, else the smaller
  *          of need and the bias held,
- *   code = e4m3(clamp(x 2^bias)) to nearest even (NaN stays NaN);
+ *   code = e4m3(clamp(x 2^bias)) to nearest even (NaN stays NaN), clamped to
+ *          448, and to 240 for bias -120, the least that a value asks for:
+ *          what is held is finite in bf16;
  * where the bias held falls, the codes of the block's earlier tokens are
  * rounded anew, exactly but for those that leave the normal range. Later
  * codes of the block are left as they were.
@@ -100,8 +102,7 @@ fp8_status fp8_cache_append(const fp8_cache* cache, const fp8_cache_batch* batch
                             const float* freqs, int rot, int interleaved, hipStream_t stream);
 
 /* The values of the batch's tokens as the cache holds them, to bf16 (exact
- * within its normal range; a value within 2^-4 of 2^128 may be held as that,
- * which is an infinity). */
+ * within its normal range). */
 fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, const fp8_cache_rows* k,
                           const fp8_cache_rows* v, hipStream_t stream);
 
@@ -110,9 +111,11 @@ fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, 
  * own tokens already. The query at position p sees positions j <= p, and
  * j > p - window if window > 0. Query head a reads head a / (q_heads /
  * heads) of the cache.
- *   s = scale q . k;  if softcap > 0: s = softcap tanh(s / softcap);
+ *   s = scale q . k, |scale| <= 2^64;
+ *   if softcap > 0 (2^-64 .. 2^64): s = softcap tanh(s / softcap);
  *   out = sum over the seen of softmax(s) v,  lse = log(sum of exp(s)).
- * Where nothing is seen, or only scores of -inf, out is 0 and lse -inf. Keys
+ * Where nothing is seen, or only scores of -inf, out is 0 and lse -inf.
+ * Positions from 2^31 - 256 on are not seen. out may be q itself. Keys
  * and values enter the products exactly, sums and the softmax are 32-bit, out
  * is bf16 (any strides), lse fp32 [tokens, q_heads] or NULL. Weights enter as
  * two bf16 each, 2^-17 off, so that out is as far off as its own rounding;

@@ -26,7 +26,7 @@
 // many as the chip holds at once: whatever the lengths, all CUs end together.
 // A tile cut by a share's end leaves its parts' sums in the workspace, and a
 // second launch joins them. Many rows (prompts): one workgroup a tile, the
-// longest first.
+// longest first; of still more, one wave a tile.
 #include "cache.h"
 
 namespace fp8lin {
@@ -81,9 +81,11 @@ __device__ inline float tanh_(float x) {
   return __builtin_fabsf(x) < 0.25f ? near : t;
 }
 
-// bytes of w that are codes of NaN, as 0xFF
-__device__ inline uint32_t nan_bytes(uint32_t w) {
-  const uint32_t m = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+// Bytes of w, as 0xFF, that are codes of NaN; of scale 2^120 also those beyond
+// bf16: a block holds none, but for what an earlier use of its page left
+// behind the last token.
+__device__ inline uint32_t nan_bytes(uint32_t w, float scale) {
+  const uint32_t m = (((w & 0x7F7F7F7Fu) + (scale < 0x1p120f ? 0x01010101u : 0x08080808u)) & 0x80808080u) >> 7;
   return m * 0xFFu;
 }
 __device__ inline float lse_of(float m, float sum) {
@@ -188,7 +190,7 @@ struct Scores {
 };
 __device__ inline Scores scores_of(const CacheAttend& a, bool cap) {
   const float scale = a.scale == 0 ? 1.0f : __builtin_fabsf(a.scale);
-  return {cap ? 1.0f : scale * kLog2e, cap ? scale / a.cap : 0.0f, cap ? a.cap * kLog2e : 0.0f,
+  return {cap ? 1.0f : scale * kLog2e, cap ? __builtin_fminf(scale / a.cap, 0x1p127f) : 0.0f, cap ? a.cap * kLog2e : 0.0f,
           a.scale < 0 ? 0x80008000u : 0u, a.scale == 0 ? 0u : 0xFFFFFFFFu};
 }
 
@@ -260,7 +262,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
       seen[r] = 0;
       int at = pos[r];
       asm volatile("" : "+v"(at));  // computed here: every step would pay for the selects
-      const int low = a.window > 0 ? at - a.window : -1;
+      const int low = a.window > 0 && at >= a.window ? at - a.window : -1;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
@@ -323,7 +325,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) any |= nan_bytes(c.w[b][i][n]);
+        for (int n = 0; n < 4; ++n) any |= nan_bytes(c.w[b][i][n], s8.v[b]);
     if (__any(any != 0)) {
       // found anew: 32 registers less than held from the search
 #pragma unroll
@@ -333,7 +335,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
         uint32_t n[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          n[b] = nan_bytes(c.w[b][i / 4][i % 4]);
+          n[b] = nan_bytes(c.w[b][i / 4][i % 4], s8.v[b]);
           c.w[b][i / 4][i % 4] &= ~n[b];
           n[b] &= 0x38383838u;  // 1
         }
@@ -380,7 +382,7 @@ __device__ inline void walk(const CacheAttend& a, const Scores& sc, const Tile& 
     const Scales s8 = scales_of(bl, n & 31);
     if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * step, to, step, lane);
     // hidden from somebody: the rows' positions are first .. last
-    const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && j0 <= t.last - a.window)));
+    const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && t.last >= a.window && j0 <= t.last - a.window)));
     attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, query, lane >> 4, s8, k, v, st, next_k, next_v);
   }
 }
@@ -547,14 +549,22 @@ __device__ inline Units units_of(const CacheAttend& a, const Seq& s, int shift) 
   return {(s.n * a.group + R - 1) / R, (int)((p.to - p.from + (kStep << shift) - 1) >> (kStepLog + shift)) + kBegin, p.from};
 }
 
-// sum over the lanes up to this one
+// Sum over the lanes up to this one, of values up to kMostUnits and no more
+// than that: all that a batch can have, so that whatever starts holds
+// (decreasing ones count rows twice) no place is outside of it.
+constexpr int kMostUnits = 1 << 30;
+__device__ inline int least(int a, int b) { return a < b ? a : b; }
 __device__ inline int scan(int x) {
-  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // row_shr:1
-  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
-  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  const auto add = [](int a, int b) {
+    const uint32_t s = (uint32_t)a + (uint32_t)b;
+    return (int)(s < (uint32_t)kMostUnits ? s : (uint32_t)kMostUnits);
+  };
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true));   // row_shr:1
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true));
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true));
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true));
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));  // row_bcast:15 into rows 1 and 3
+  x = add(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));  // row_bcast:31 into rows 2 and 3
   return x;
 }
 
@@ -570,10 +580,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_shares_kernel(
   for (int i = lane * per; i < (lane + 1) * per && i < a.b.sequences; ++i) {
     s = seq_of(a.b, i);
     const Units n = units_of<R>(a, s, shift);
-    mine += n.tiles * a.c.heads * n.units;
+    mine = least(mine + n.tiles * a.c.heads * n.units, kMostUnits);
   }
   const int upto = scan(mine), total = __builtin_amdgcn_readlane(upto, 63);
-  const int share = (int)(((int64_t)total + kShares - 1) / kShares);
+  const int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   int u = blockIdx.x * share;
   const int end = total - u < share ? total : u + share;
   int4 open = {0, 0, 0, 0};
@@ -586,7 +596,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_shares_kernel(
     bool known = per == 1, found = false;  // s is seq's; and the place in its tiles
     Units n = {0, 0, 0};
     int k0 = 0, at = 0, h = 0;
-    while (u < end) {
+    while (u < end && seq < a.b.sequences) {
       if (!found) {
         if (!known) s = uni(seq_of(a.b, seq));
         known = false;
@@ -646,6 +656,7 @@ __global__ __launch_bounds__(64 * kWaves) void cache_attention_join_kernel(Cache
   __shared__ float ml[kWaves][2][64];
   const int4 open = ws.heads[blockIdx.x];
   if (open.x == 0) return;
+  const int parts = open.x < (int)(gridDim.x - blockIdx.x) ? open.x : (int)(gridDim.x - blockIdx.x);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Seq s = seq_of(a.b, open.y);
   const int row = (blockIdx.y * 256 + 4 * lane) / D, d = (blockIdx.y * 256 + 4 * lane) % D;
@@ -656,7 +667,7 @@ __global__ __launch_bounds__(64 * kWaves) void cache_attention_join_kernel(Cache
   bq_f32x4 o = {0, 0, 0, 0};
   // wave w: parts w, w + 4, ..; each part's sum, scaled to the running maximum
   if (have)
-    for (int p = wave; p < open.x; p += kWaves) {
+    for (int p = wave; p < parts; p += kWaves) {
       const int64_t slot = p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p);
       const float mp = ws.sums[(slot * R + row) * 2], lp = ws.sums[(slot * R + row) * 2 + 1];
       const bq_f32x4 x = *(const bq_f32x4*)(ws.parts + (slot * R + row) * D + d);
@@ -775,6 +786,7 @@ struct Form {
   bool tiles;
   int64_t count;  // of tiles, at most
   int shift;      // of a unit
+  int shares;     // workgroups: no more than there can be units
 };
 constexpr int most_rows(int head_dim) { return head_dim == 256 ? 2 : 4; }  // 16-row tiles, by a wave's registers
 Form form_of(const CacheAttend& a, int head_dim) {
@@ -785,7 +797,9 @@ Form form_of(const CacheAttend& a, int head_dim) {
   int64_t most = a.b.table_pages << a.c.shift;
   most = most < kMostTokens ? most : kMostTokens;
   f.shift = 0;
-  while (f.count * ((most + kStep) / ((int64_t)kStep << f.shift) + 1 + kBegin) >= (int64_t)1 << 30 && f.shift < 23) ++f.shift;
+  const auto units = [&] { return f.count * ((most + kStep) / ((int64_t)kStep << f.shift) + 1 + kBegin); };
+  while (units() >= kMostUnits && f.shift < 23) ++f.shift;
+  f.shares = units() < kShares ? (int)units() : kShares;
   f.tiles = a.b.starts && rows > 32 && f.count >= 2 * kShares;
   return f;
 }
@@ -816,12 +830,12 @@ hipError_t run(const CacheAttend& a, const Form& f, const Space& ws, hipStream_t
       return hipGetLastError();
     }
   }
-  if (a.cap > 0) cache_attention_shares_kernel<D, MT, true><<<kShares, block, 0, st>>>(a, ws, f.shift);
-  else cache_attention_shares_kernel<D, MT, false><<<kShares, block, 0, st>>>(a, ws, f.shift);
+  if (a.cap > 0) cache_attention_shares_kernel<D, MT, true><<<f.shares, block, 0, st>>>(a, ws, f.shift);
+  else cache_attention_shares_kernel<D, MT, false><<<f.shares, block, 0, st>>>(a, ws, f.shift);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int rows = !a.b.starts && a.group < 16 * MT ? a.group : 16 * MT;
-  cache_attention_join_kernel<D, MT><<<dim3(kShares, (rows * D + 255) / 256), block, 0, st>>>(a, ws);
+  cache_attention_join_kernel<D, MT><<<dim3(f.shares, (rows * D + 255) / 256), block, 0, st>>>(a, ws);
   return hipGetLastError();
 }
 

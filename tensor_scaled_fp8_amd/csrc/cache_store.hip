@@ -43,13 +43,17 @@ __device__ inline uint32_t need_byte(uint32_t mag, bool inf) {
   uint32_t s = mag ? scale_byte<FP8_E4M3>(mag) : 1u;
   return inf ? umax(s, 127u) : s;
 }
-__device__ inline float clamp448(float f, float scale) {
-  const float m = 448.0f * scale;
+// Clamped to the format's largest value; of scale 2^120, the largest there is,
+// to 240: what is held is finite in bf16, so that a hidden token's weight of 0
+// leaves 0 of it.
+constexpr float kTopScale = 0x1p120f;
+__device__ inline float clamped(float f, float scale) {
+  const float m = scale < kTopScale ? 448.0f * scale : 240.0f * kTopScale;
   return f != f ? f : fminf(fmaxf(f, -m), m);
 }
-// codes of four values; beyond the format's largest only if an infinity is among them
+// codes of four values; beyond the largest only if an infinity is among them or of the largest scale
 __device__ inline uint32_t codes_of(float a, float b, float c, float d, float s, bool inf) {
-  if (inf) return code4<FP8_E4M3>(clamp448(a, s), clamp448(b, s), clamp448(c, s), clamp448(d, s), s);
+  if (inf || s >= kTopScale) return code4<FP8_E4M3>(clamped(a, s), clamped(b, s), clamped(c, s), clamped(d, s), s);
   return code4<FP8_E4M3>(a, b, c, d, s);
 }
 // codes of scale s0 rounded anew to scale s1

@@ -48,6 +48,8 @@ struct Fp4Form {
   int cols;             // of Y a workgroup (fused, few)
 };
 Fp4Form fp4_form(int64_t M, int64_t K, int64_t N);
+// Y of an empty sum (K = 0): the product's kernels have no block of K to stand on
+hipError_t launch_fp4_zero(uint16_t* y, int64_t n, hipStream_t st);
 hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
 hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
 

@@ -433,7 +433,17 @@ hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* 
   return f.nb == 2 ? run_many<MF, 2>(x, w, f, y, st) : run_many<MF, 3>(x, w, f, y, st);
 }
 
+__global__ __launch_bounds__(256) void fp4_zero_kernel(uint16_t* __restrict__ y, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) y[i] = 0;
+}
+
 }  // namespace
+
+hipError_t launch_fp4_zero(uint16_t* y, int64_t n, hipStream_t st) {
+  if (n == 0) return hipSuccess;
+  fp4_zero_kernel<<<(unsigned)(n < 2048 * 256 ? (n + 255) / 256 : 2048), 256, 0, st>>>(y, n);
+  return hipGetLastError();
+}
 
 // X's values in bf16 fit 64 KB of LDS
 bool fp4_fused(int64_t M, int64_t K) { return M <= 16 && M * fp4_xblocks(K) <= 248; }

@@ -131,8 +131,8 @@ fp8_status fp8_cache_attention(const fp8_cache* cache, const fp8_cache_batch* ba
                                float scale, float softcap, int window, const fp8_cache_rows* out, float* lse, void* ws,
                                size_t ws_bytes, hipStream_t stream) {
   if (!cache_ok(cache) || !batch_ok(batch) || !rows_ok(q, batch->tokens) || !rows_ok(out, batch->tokens) ||
-      !q_heads_ok(q_heads, cache->heads) || !(softcap >= 0.0f && softcap < __builtin_inff()) || window < 0 ||
-      !(__builtin_fabsf(scale) < __builtin_inff()) || !aligned(lse, 4) || !aligned(ws, 16))
+      !q_heads_ok(q_heads, cache->heads) || !(softcap == 0.0f || (softcap >= 0x1p-64f && softcap <= 0x1p64f)) || window < 0 ||
+      !(__builtin_fabsf(scale) <= 0x1p64f) || !aligned(lse, 4) || !aligned(ws, 16))
     return FP8_ERR_INVALID;
   if (!attend_fits(batch, q_heads)) return FP8_ERR_UNSUPPORTED;
   CacheAttend a = attend_of(cache, batch, q_heads);
@@ -196,6 +196,7 @@ fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t 
   if (need && (!scratch || scratch_bytes < need)) return FP8_ERR_INVALID;
   const Bf16Mat x = {(const uint16_t*)X, ldx, M, K};
   const Fp4Mat w = {(uint8_t*)codes, (uint8_t*)scales, K, N};
+  if (K == 0) return hip_status(launch_fp4_zero((uint16_t*)Y, M * N, stream));
   if (fp4_fused(M, K)) return hip_status(launch_fp4_fused(x, w, (uint16_t*)Y, stream));
   const Fp4Scratch s(scratch, M, K);
   const hipError_t e = launch_fp4_x(x, s.x, stream);

@@ -6,6 +6,7 @@
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
 
+#include <cmath>
 #include <optional>
 
 #include "fp8lin_serve.h"
@@ -147,6 +148,7 @@ Maybe append(const Tensor& data, int64_t pages, int64_t page_tokens, int64_t hea
   no_grad(k, "k");
   no_grad(v, "v");
   if (q) no_grad(*q, "q");
+  if (freqs) no_grad(*freqs, "freqs");
   on_device(data, "cache");
   on(k, data, "k");
   on(v, data, "v");
@@ -195,8 +197,8 @@ std::pair<Tensor, Maybe> attention(const Tensor& data, int64_t pages, int64_t pa
   const int64_t q_heads = q.size(1);
   const fp8_cache_batch b = batch_of(tables, lengths, starts, tokens);
   if (given) rows_of(*given, tokens, q_heads, head_dim, "out", true);
-  if (!(softcap >= 0) || !std::isfinite((float)softcap)) refuse("softcap must be finite and not negative");
-  if (!std::isfinite((float)scale)) refuse("scale must be finite");
+  if (!(softcap == 0 || (softcap >= 0x1p-64 && softcap <= 0x1p64))) refuse("softcap must be 0 or between 2^-64 and 2^64");
+  if (!(std::fabs(scale) <= 0x1p64)) refuse("scale must be finite, up to 2^64");
   if (window < 0 || window > INT32_MAX) refuse("window must be between 0 and 2^31 - 1");
   no_grad(q, "q");
   on_device(data, "cache");
@@ -263,6 +265,9 @@ Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, cons
     bf16(*given, "Y");
     if (given->dim() != 2 || given->size(0) != M || given->size(1) != N || !given->is_contiguous())
       refuse("Y must be contiguous [" + std::to_string(M) + ", " + std::to_string(N) + "], got " + shape_of(*given));
+    // X is read until the last workgroup ends
+    const char *x0 = (const char*)ptr(X), *y0 = (const char*)ptr(*given);
+    if (x0 && y0 && x0 < y0 + 2 * M * N && y0 < x0 + 2 * ((M - 1) * X.stride(0) + K)) refuse("Y must not overlap X");
   }
   no_grad(X, "X");
   on_device(X, "X");

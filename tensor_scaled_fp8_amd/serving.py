@@ -29,7 +29,7 @@ from typing import Optional, Tuple
 import torch
 
 from .binding import _at
-from .block import BlockInferenceLinear, _as_rows, _binding
+from .block import BlockInferenceLinear, _as_rows, _binding, _wants_grad
 from ._lib import load
 
 _U8 = torch.uint8
@@ -108,8 +108,8 @@ def fp8_cache_attention(q: torch.Tensor, cache: BlockKVCache, tables: torch.Tens
     which holds these tokens' own keys and values already. The query at
     position p sees positions j <= p, and j > p - window if window > 0. Scores
     are scale (default head_dim^-0.5) q . k, then softcap tanh(score / softcap)
-    if softcap > 0. Returns [tokens, heads of q, head_dim], 0 where nothing is
-    seen; with lse also the logarithms of the sums, float32 [tokens, heads of
+    if softcap > 0. Returns [tokens, heads of q, head_dim] (in out, which may be
+    q, if given), 0 where nothing is seen; with lse also the logarithms of the sums, float32 [tokens, heads of
     q], -inf there."""
     if scale is None:
         scale = cache.head_dim ** -0.5
@@ -157,7 +157,8 @@ def prepare_fp4_weight(W: torch.Tensor) -> FP4Tensor:
 
 def fp4_linear_fwd_cached(X: torch.Tensor, w: FP4Tensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [M, N] = X [M, K] W from a stored 4-bit weight (prepare_fp4_weight);
-    X is quantised to E4M3, a scale for each 128 elements of a row."""
+    X is quantised to E4M3, a scale for each 128 elements of a row. Y, if
+    given, is contiguous and does not overlap X."""
     return _call(X, "fp4_serve", X, w.data, w.K, w.N, Y)
 
 
@@ -179,7 +180,8 @@ class InferenceAttention(torch.nn.Module):
     keys and values, rotation and append, attention, output projection. Wqkv
     [hidden, (heads + 2 kv_heads) head_dim] (queries, keys, values) and Wo
     [heads head_dim, hidden] are stored once, in 8 bits (a scale for each 128
-    elements) or 4 (for each 32)."""
+    elements) or 4 (for each 32). Like them freqs stay as they are, float32,
+    when the module's type is changed."""
 
     def __init__(self, Wqkv: torch.Tensor, Wo: torch.Tensor, heads: int, kv_heads: int, head_dim: int,
                  freqs: Optional[torch.Tensor] = None, interleaved: bool = False, scale: Optional[float] = None,
@@ -191,17 +193,25 @@ class InferenceAttention(torch.nn.Module):
                              f"heads of {head_dim}")
         if bits not in (4, 8):
             raise ValueError(f"weights are stored in 4 or 8 bits, got {bits}")
+        if freqs is not None and (freqs.dtype is not torch.float32 or freqs.dim() != 1):
+            raise ValueError(f"freqs must be float32 and 1-D, got {freqs.dtype} {tuple(freqs.shape)}")
         linear = FP4InferenceLinear if bits == 4 else BlockInferenceLinear
         self.qkv, self.out = linear(Wqkv.detach()), linear(Wo.detach())
-        self.register_buffer("freqs", freqs)
+        self.register_buffer("freq_bytes", None if freqs is None else freqs.detach().contiguous().view(_U8))
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.interleaved, self.scale, self.softcap, self.window = interleaved, scale, softcap, window
+
+    @property
+    def freqs(self) -> Optional[torch.Tensor]:
+        return None if self.freq_bytes is None else self.freq_bytes.view(torch.float32)
 
     def forward(self, x: torch.Tensor, cache: BlockKVCache, tables: torch.Tensor, lengths: torch.Tensor,
                 starts: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [tokens, hidden]: appends the tokens' keys and values to the cache and returns [tokens, out features]."""
         if x.dim() != 2:
             raise ValueError(f"x must be [tokens, hidden], got {tuple(x.shape)}")
+        if _wants_grad(x):
+            raise NotImplementedError("x wants a gradient: the serving operators have none (use torch.no_grad())")
         h, g, d = self.heads, self.kv_heads, self.head_dim
         qkv = self.qkv(x).view(-1, h + 2 * g, d)
         q, k, v = qkv[:, :h], qkv[:, h:h + g], qkv[:, h + g:]

@@ -81,8 +81,10 @@ class Model:
                             if bias < was:
                                 old = self.codes[w, page, base:base + first, h]
                                 old[:] = encode(VALUES[old] * (0.0 if was == 127 else 2.0 ** (bias - was)), E4M3)
+                        most = 240.0 if bias == -120 else 448.0                       # finite in bf16
                         with np.errstate(over="ignore"):
-                            self.codes[w, page, base + first:base + first + len(rows), h] = encode(x[:, h] * 2.0 ** bias, E4M3)
+                            y = np.clip(x[:, h] * 2.0 ** bias, -most, most)
+                        self.codes[w, page, base + first:base + first + len(rows), h] = encode(y, E4M3)
                         self.bias[w, page, blk, h] = bias
 
     def values(self, w, table, pos):

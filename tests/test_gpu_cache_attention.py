@@ -146,6 +146,34 @@ def test_extreme_scores():
     assert np.isnan(out[4, 0]).all() and np.isfinite(np.delete(out.reshape(12, d), 8, axis=0)).all()
 
 
+@pytest.mark.parametrize("new,hq", [(1, 6), (40, 6), (40, 2)])
+def test_largest_values_in_hidden_places(new, hq):
+    """bf16's largest values that a window or the order of tokens hides, and codes that an earlier sequence left behind the
+    last token of a block whose scale is the largest, change no bit."""
+    g = np.random.Generator(np.random.PCG64(60 + new + hq))
+    heads, d, n, most = 2, 64, 100, 255 / 128 * 2.0 ** 127
+    k, v, q = draw(g, (n, heads, d), 1), draw(g, (n, heads, d), 1), up(draw(g, (new, hq, d), 1))
+    how, hidden = (dict(window=20), slice(64, 80)) if new == 1 else (dict(), slice(96, 100))
+    outs = []
+    for far in (False, True):
+        if far:
+            v[hidden] = most * np.sign(v[hidden])
+        cache, model, tables = filled(np.random.Generator(np.random.PCG64(1)), [n], heads, d, 16, k, v)
+        outs.append(tsf.fp8_cache_attention(q, cache, ints(tables), ints([n]), ints([0, new]), **how))
+    rows = slice(0, new - (0 if new == 1 else 4))         # those that see none of them
+    assert torch.isfinite(outs[0]).all() and torch.equal(outs[0][rows], outs[1][rows])
+    # the same pages for a shorter sequence, with a value of the largest scale, and pages that are new
+    v[33, :, 5] = most
+    new = min(new, 35)
+    fresh = tsf.BlockKVCache(cache.pages, 16, heads, d, device="cuda")
+    for c in (cache, fresh):
+        if c is cache:
+            c.data[:c.pages * 16 * heads * d * 2] = 126                                 # the largest code everywhere
+        tsf.fp8_cache_append(c, up(k[:35]), up(v[:35]), ints(tables), ints([35]), ints([0, 35]))
+    outs = [tsf.fp8_cache_attention(q[:new], c, ints(tables), ints([35]), ints([0, new])) for c in (cache, fresh)]
+    assert torch.equal(outs[0][..., :5], outs[1][..., :5]) and torch.isfinite(outs[0][..., :5]).all()
+
+
 def test_strides_streams_and_equal_bits():
     g = np.random.Generator(np.random.PCG64(10))
     lens, hq, d = [300, 45], 8, 128

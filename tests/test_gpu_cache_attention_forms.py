@@ -58,6 +58,9 @@ def test_form(case, how):
     out, lse = tsf.fp8_cache_attention(q, cache, ints(tables), ints(lens), ints(starts), lse=True, **how)
     again = tsf.fp8_cache_attention(q, cache, ints(tables), ints(lens), ints(starts), **how)
     assert torch.equal(out, again)
+    place = q.clone()                            # in place
+    assert tsf.fp8_cache_attention(place, cache, ints(tables), ints(lens), ints(starts), out=place, **how) is place
+    assert torch.equal(out, place)
     out, lse, rk, rv, q = host(out), lse.cpu().numpy().astype(np.float64), host(rk), host(rv), host(q)
     # every sequence's first and last row, and others, of the first and last head and others
     for i, (length, n) in enumerate(zip(lens, new)):

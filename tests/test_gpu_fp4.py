@@ -157,7 +157,9 @@ def test_empty():
     w = tsf.prepare_fp4_weight(torch.ones((64, 48), **bf))
     assert tsf.fp4_linear_fwd_cached(torch.ones((0, 64), **bf), w).shape == (0, 48)
     w = tsf.prepare_fp4_weight(torch.ones((0, 48), **bf))
-    assert (tsf.fp4_linear_fwd_cached(torch.ones((3, 0), **bf), w) == 0).all()
+    for M in (3, 20, 70, 1000):
+        y = torch.full((M, 48), 5.0, **bf)
+        assert (tsf.fp4_linear_fwd_cached(torch.ones((M, 0), **bf), w, y) == 0).all()
     w = tsf.prepare_fp4_weight(torch.ones((64, 0), **bf))
     assert tsf.fp4_linear_fwd_cached(torch.ones((3, 64), **bf), w).shape == (3, 0)
     assert w.dequantize().shape == (64, 0)

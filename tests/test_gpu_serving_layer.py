@@ -55,6 +55,30 @@ def test_prompt_then_decode(bits, hq, hk, d, inter):
         assert np.isfinite(host(y)).all()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_layer_refuses_gradients_and_keeps_its_angles(bits):
+    g = np.random.Generator(np.random.PCG64(8))
+    K, hq, hk, d = 128, 2, 1, 64
+    bf = [up(to_bf16(g.standard_normal(s) * 0.06)) for s in ((K, (hq + 2 * hk) * d), (hq * d, K))]
+    layer = tsf.InferenceAttention(*bf, hq, hk, d, freqs=torch.from_numpy(freqs_of(d)).cuda(), bits=bits)
+    a = (tsf.BlockKVCache(1, 16, hk, d, device="cuda"), ints([[0]]), ints([5]), ints([0, 5]))
+    x = up(g.standard_normal((5, K)))
+    want = layer(x, *a)
+    x.requires_grad_()
+    with pytest.raises(NotImplementedError, match="x wants a gradient"):
+        layer(x, *a)
+    with torch.no_grad():
+        assert torch.equal(layer(x, *a), want)
+    layer.to(torch.bfloat16)
+    assert layer.freqs.dtype == torch.float32
+    with torch.inference_mode():
+        assert torch.equal(layer(x.detach(), *a), want)
+    other = tsf.InferenceAttention(*bf, hq, hk, d, freqs=torch.zeros(d // 2, device="cuda"), bits=bits)
+    other.load_state_dict(layer.state_dict())
+    with torch.no_grad():
+        assert torch.equal(other(x, *a), want)
+
+
 def test_layer_in_a_graph():
     """A captured decode step of a padded batch, replayed as sequences come and go."""
     g = np.random.Generator(np.random.PCG64(5))

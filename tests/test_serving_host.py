@@ -82,7 +82,7 @@ def test_rows_and_numbers_that_are_refused():
     assert calls(freqs=None, **bad)[0] == INV and calls(freqs=OK + 2, **bad)[0] == INV
     assert calls(q_heads=3, **bad)[::2] == (INV, INV)
     nan, inf = float("nan"), float("inf")
-    for how in (dict(scale=nan), dict(scale=inf), dict(cap=-1.0), dict(cap=nan), dict(cap=inf), dict(window=-1), dict(lse=OK + 2),
+    for how in (dict(scale=nan), dict(scale=inf), dict(cap=-1.0), dict(cap=nan), dict(cap=inf), dict(cap=1e-20), dict(cap=1e20), dict(scale=-1e20), dict(window=-1), dict(lse=OK + 2),
                 dict(ws=OK + 8)):
         assert calls(**how, **bad)[2] == INV, how
     lib, r = tsf.load(), ctypes.byref
@@ -219,6 +219,7 @@ def test_appends_that_are_refused(change, said):
 
 @pytest.mark.parametrize("change,said", BATCHES + [
     (dict(q=z(4, 4, 64)), "one row a sequence"), (dict(scale=float("nan")), "scale must be"), (dict(scale=1e39), "scale must be"),
+    (dict(scale=-1e20), "scale must be"), (dict(softcap=1e-20), "softcap must be"), (dict(softcap=1e20), "softcap must be"),
     (dict(softcap=-1.0), "softcap must be"), (dict(softcap=float("inf")), "softcap must be"), (dict(window=-1), "window must be"),
     (dict(window=2 ** 31), "window must be"), (dict(out=z(3, 4, 64, dtype=torch.float32)), "out must be"),
     (dict(out=z(3, 1, 64).expand(3, 4, 64)), "expanded")])
@@ -237,7 +238,7 @@ def test_reads_that_are_refused():
 
 
 def test_gradients_are_refused():
-    for name in ("k", "v", "q"):
+    for name in ("k", "v", "q", "freqs"):
         with pytest.raises(NotImplementedError, match=f"{name} wants a gradient"):
             append(**{name: GOOD[name]().requires_grad_()})
         with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
@@ -265,6 +266,10 @@ def test_fp4_that_is_refused():
                        ((z(2, 512), w), "device tensor")):
         with pytest.raises(ValueError, match=said):
             tsf.fp4_linear_fwd_cached(*args)
+    square, x = tsf.FP4Tensor(torch.zeros(4 * 4352 * 8, dtype=U8), 512, 512), z(2 * 512 + 1)
+    for y in (x[:-1], x[1:]):
+        with pytest.raises(ValueError, match="overlap"):
+            tsf.fp4_linear_fwd_cached(x[:-1].view(2, 512), square, y.view(2, 512))
     with pytest.raises(ValueError, match="device tensor"):
         w.dequantize()
     for bad, said in ((z(2, 3, 4), "2-D"), (z(4, 4, dtype=torch.float32), "bfloat16"), (z(4, 4), "device tensor")):
@@ -275,6 +280,9 @@ def test_fp4_that_is_refused():
             tsf.InferenceAttention(*args)
     with pytest.raises(ValueError, match="4 or 8 bits"):
         tsf.InferenceAttention(z(8, 4 * 64), z(128, 8), 2, 1, 64, bits=5)
+    for freqs in (torch.zeros(32, dtype=torch.float64), torch.zeros(1, 32)):
+        with pytest.raises(ValueError, match="freqs must be float32"):
+            tsf.InferenceAttention(z(8, 4 * 64), z(128, 8), 2, 1, 64, freqs=freqs)
 
 
 def test_calls_run_on_their_tensors_device(monkeypatch):
