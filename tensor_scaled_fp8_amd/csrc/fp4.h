@@ -36,10 +36,12 @@ inline size_t fp4_x_scales(int64_t M, int64_t K) { return (size_t)((M + 15) / 16
 hipError_t launch_fp4_x(const Bf16Mat& x, const Fp4X& q, hipStream_t st);
 
 // Y [M, N] = X W. Of few rows (and blocks of K) X is quantised by the
-// product's own launch; otherwise it comes quantised. Up to kFp4Few rows the
-// product is of bf16 operands, exact but for FP32 sums, since it waits for W's
-// bytes all the same (64 rows by 4096 x 12288: FEW_64 us; by the 8-bit
-// instructions FEW_64_8); of more, of the 8-bit and 4-bit codes.
+// product's own launch; otherwise it comes quantised. Up to kFp4Few rows (a
+// decode batch) the product is of bf16 operands, exact but for FP32 sums, for
+// the sake of what a later 8-bit rounding makes of it; of more, of the 8-bit
+// and 4-bit codes. By 4096 x 12288 and 8192 x 8192, us: 20 rows 13.5 and 17.3
+// (by the 8-bit instructions 14.0 and 20.7), 32 rows 14.2 and 17.6 (14.3 and
+// 21.0), 64 rows 18.5 and 24.1 (14.8 and 22.6).
 constexpr int64_t kFp4Few = 64;
 bool fp4_fused(int64_t M, int64_t K);
 struct Fp4Form {
