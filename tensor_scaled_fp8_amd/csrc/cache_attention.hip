@@ -185,12 +185,18 @@ __device__ inline void load_codes(const CacheAttend& a, const Blocks& bl, int n,
 // scale of 0 they are 0, so that unit is above 0 and the largest score is the
 // largest product's.
 struct Scores {
-  float unit, per_cap, cap_log2;
+  float unit, per_cap, cap_log2, twice;  // twice: 2 log2(e) per_cap, or 0 for a cap above kNearCap
   uint32_t flip, keep;  // of the queries' bits
 };
+// Up to this cap 1 - 2 / (exp(2 x) + 1) is near enough for tanh near 0 too:
+// 3 2^-24 off, of a score 2^-16, a weight's own rounding. It takes 3
+// instructions for the 13 of tanh_ (drafted tokens under a window and a cap of
+// 50: 29.5 us by that one, 27.2).
+constexpr float kNearCap = 64.0f;
 __device__ inline Scores scores_of(const CacheAttend& a, bool cap) {
   const float scale = a.scale == 0 ? 1.0f : __builtin_fabsf(a.scale);
-  return {cap ? 1.0f : scale * kLog2e, cap ? __builtin_fminf(scale / a.cap, 0x1p127f) : 0.0f, cap ? a.cap * kLog2e : 0.0f,
+  const float per_cap = cap ? __builtin_fminf(scale / a.cap, 0x1p120f) : 0.0f;
+  return {cap ? 1.0f : scale * kLog2e, per_cap, cap ? a.cap * kLog2e : 0.0f, a.cap <= kNearCap ? 2.0f * kLog2e * per_cap : 0.0f,
           a.scale < 0 ? 0x80008000u : 0u, a.scale == 0 ? 0u : 0xFFFFFFFFu};
 }
 
@@ -248,12 +254,22 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
   if (MT > 1) __builtin_amdgcn_s_setprio(0);
   next_k();
   if constexpr (CAP) {
+    if (sc.twice > 0) {
 #pragma unroll
-    for (int r = 0; r < MT; ++r)
+      for (int r = 0; r < MT; ++r)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[r][b][i] = sc.cap_log2 * tanh_(x[r][b][i] * sc.per_cap);
+          for (int i = 0; i < 4; ++i)
+            x[r][b][i] = __builtin_fmaf(-2.0f * sc.cap_log2, __builtin_amdgcn_rcpf(exp2_(x[r][b][i] * sc.twice) + 1.0f), sc.cap_log2);
+    } else {
+#pragma unroll
+      for (int r = 0; r < MT; ++r)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[r][b][i] = sc.cap_log2 * tanh_(x[r][b][i] * sc.per_cap);
+    }
   }
   uint32_t seen[MT];  // bit i: the row sees token i of the lane's 8
   if (hard) {
@@ -786,8 +802,17 @@ struct Form {
   bool tiles;
   int64_t count;  // of tiles, at most
   int shift;      // of a unit
-  int shares;     // workgroups: no more than there can be units
+  int most;       // workgroups that share the work
+  int shares;     // no more of them than there can be units
 };
+// Workgroups that share the work: two a CU, by their registers, and three of
+// tiles of 16 rows of up to 128 elements if every CU has a tile. With fewer, of
+// long sequences, the third only cuts them up further (us of one decoded token
+// with two and three a CU, by sequences, lengths, query and key heads: 100 of
+// 10 to 3000, 10 and 10 of 128 elements 38.8 and 35.7, of 64 30.9 and 26.2; 64
+// of 100 to 16000, 32 and 4 of 128 47.1 and 44.6, of 64 31.2 and 30.0; 8 of
+// 100 to 3000, 64 and 8 of 128 13.9 and 15.2).
+int most_shares(int head_dim, int mt, int64_t tiles) { return mt == 1 && head_dim <= 128 && tiles >= 256 ? kShares * 3 / 2 : kShares; }
 constexpr int most_rows(int head_dim) { return head_dim == 256 ? 2 : 4; }  // 16-row tiles, by a wave's registers
 Form form_of(const CacheAttend& a, int head_dim) {
   const int64_t rows = a.b.starts ? ((int64_t)a.b.tokens * a.group + a.b.sequences - 1) / a.b.sequences : a.group;
@@ -799,18 +824,19 @@ Form form_of(const CacheAttend& a, int head_dim) {
   f.shift = 0;
   const auto units = [&] { return f.count * ((most + kStep) / ((int64_t)kStep << f.shift) + 1 + kBegin); };
   while (units() >= kMostUnits && f.shift < 23) ++f.shift;
-  f.shares = units() < kShares ? (int)units() : kShares;
+  f.most = most_shares(head_dim, f.mt, f.count);
+  f.shares = units() < f.most ? (int)units() : f.most;
   f.tiles = a.b.starts && rows > 32 && f.count >= 2 * kShares;
   return f;
 }
 constexpr int64_t kRowsTiles = 5 * kShares;  // of waves that take whole tiles: more than a round of them
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-Space space_of(void* ws, int mt, int head_dim, size_t* bytes) {
-  const size_t rows = (size_t)2 * kShares * 16 * mt;
+Space space_of(void* ws, const Form& f, int head_dim, size_t* bytes) {
+  const size_t rows = (size_t)2 * f.most * 16 * f.mt;
   uint8_t* p = (uint8_t*)ws;
   const size_t parts = round256(rows * head_dim * 4), sums = round256(rows * 8);
-  *bytes = parts + sums + kShares * sizeof(int4);
+  *bytes = parts + sums + f.most * sizeof(int4);
   return {(float*)p, (float*)(p + parts), (int4*)(p + parts + sums)};
 }
 
@@ -845,7 +871,7 @@ size_t cache_attention_ws_bytes(const CacheAttend& a, int head_dim) {
   if (!a.b.tokens || !a.b.sequences) return 0;
   const Form f = form_of(a, head_dim);
   size_t n = 0;
-  if (!f.tiles) space_of(nullptr, f.mt, head_dim, &n);
+  if (!f.tiles) space_of(nullptr, f, head_dim, &n);
   return n;
 }
 
@@ -863,7 +889,7 @@ hipError_t launch_cache_attention(const CacheAttend& a, int head_dim, void* ws, 
   if (!a.b.tokens || !a.b.sequences) return hipSuccess;
   const Form f = form_of(a, head_dim);
   size_t n;
-  const Space s = space_of(ws, f.mt, head_dim, &n);
+  const Space s = space_of(ws, f, head_dim, &n);
   if (f.mt == 1)
     return head_dim == 64 ? run<64, 1>(a, f, s, st) : head_dim == 128 ? run<128, 1>(a, f, s, st) : run<256, 1>(a, f, s, st);
   if (f.mt == 2)
