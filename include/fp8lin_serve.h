@@ -163,20 +163,23 @@ fp8_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t K
                           hipStream_t stream);
 /*
  * Y [M, N] (dense) = X [M, K] W on a stored 4-bit W. X is quantised as by
- * fp8_block_quantize (E4M3, a scale for each 128 of a row). Up to 64 rows the
- * products are exact and their sums 32-bit; of more rows they are
- * fp8_block_gemm's. scratch: fp4_linear_bytes (0: none is needed).
+ * fp8_block_quantize (E4M3, a scale for each 128 of a row). exact: products
+ * are exact and their sums 32-bit, for a Y that is rounded to 8 bits next.
+ * Without it products of more than 32 rows are fp8_block_gemm's, up to twice
+ * as fast and 1.5e-5 off, which a bf16 Y does not show; of fewer they are
+ * exact all the same. scratch: fp4_linear_bytes (0: none is needed).
  */
 /* How a product is cut: the kernel, its wave's 16-row and 16-column tiles and
  * the groups of waves that share K. For profiles and tests. */
 #define FP4_FUSED 0 /* X quantised by the product's launch */
 #define FP4_FEW 1   /* few rows, X quantised before */
 #define FP4_MANY 2
-fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int* form, int* row_tiles, int* col_tiles, int* groups);
+#define FP4_EXACT 3 /* many rows, exact products */
+fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int exact, int* form, int* row_tiles, int* col_tiles, int* groups);
 size_t fp4_linear_bytes(int64_t M, int64_t K, int64_t N);
 fp8_status fp4_linear_fwd_cached(const void* X_bf16, int64_t ldx, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
-                                 const uint8_t* scales, void* scratch, size_t scratch_bytes, void* Y_bf16,
-                                 hipStream_t stream);
+                                 const uint8_t* scales, int exact, void* scratch, size_t scratch_bytes,
+                                 void* Y_bf16, hipStream_t stream);
 
 #ifdef __cplusplus
 }

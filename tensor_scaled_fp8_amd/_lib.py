@@ -89,9 +89,9 @@ SIGNATURES = {
     "fp4_scales_bytes": (c_sz, [c_i64, c_i64]),
     "fp4_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "fp4_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]),
-    "fp4_linear_plan": (c_int, [c_i64, c_i64, c_i64, c_intp, c_intp, c_intp, c_intp]),
+    "fp4_linear_plan": (c_int, [c_i64, c_i64, c_i64, c_int, c_intp, c_intp, c_intp, c_intp]),
     "fp4_linear_bytes": (c_sz, [c_i64, c_i64, c_i64]),
-    "fp4_linear_fwd_cached": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "fp4_linear_fwd_cached": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_vp, c_sz, c_vp, c_vp]),
 }
 
 FP8_E4M3, FP8_E5M2 = 0, 1

@@ -36,23 +36,23 @@ inline size_t fp4_x_scales(int64_t M, int64_t K) { return (size_t)((M + 15) / 16
 hipError_t launch_fp4_x(const Bf16Mat& x, const Fp4X& q, hipStream_t st);
 
 // Y [M, N] = X W. Of few rows (and blocks of K) X is quantised by the
-// product's own launch; otherwise it comes quantised. Up to kFp4Few rows (a
-// decode batch) the product is of bf16 operands, exact but for FP32 sums, for
-// the sake of what a later 8-bit rounding makes of it; of more, of the 8-bit
-// and 4-bit codes. By 4096 x 12288 and 8192 x 8192, us: 20 rows 13.5 and 17.3
-// (by the 8-bit instructions 14.0 and 20.7), 32 rows 14.2 and 17.6 (14.3 and
-// 21.0), 64 rows 18.5 and 24.1 (14.8 and 22.6).
-constexpr int64_t kFp4Few = 64;
+// product's own launch; otherwise it comes quantised. Up to kFp4Few rows, and
+// up to kFp4FewExact of an exact product, it is of bf16 operands in the form
+// that waits for W's bytes; above, of the 8-bit and 4-bit codes, or of bf16 if
+// exact. us by 4096 x 12288 and 8192 x 8192: 32 rows 14.2 and 17.6 (of the
+// codes 14.3 and 21.0); 64 rows, exact, 18.3 and 24.3 (by the exact form of
+// many rows 19.6 and 29.7), of the codes 15.1 and 22.3.
+constexpr int64_t kFp4Few = 32, kFp4FewExact = 64;
 bool fp4_fused(int64_t M, int64_t K);
 struct Fp4Form {
-  int kind;             // FP4_FUSED, _FEW or _MANY
+  int kind;             // FP4_FUSED, _FEW, _MANY or _EXACT
   int mf, nb, groups;   // 16-row fragments of X and 16-column ones of W a wave, groups of waves over K
   int cols;             // of Y a workgroup (fused, few)
 };
-Fp4Form fp4_form(int64_t M, int64_t K, int64_t N);
+Fp4Form fp4_form(int64_t M, int64_t K, int64_t N, bool exact);
 // Y of an empty sum (K = 0): the product's kernels have no block of K to stand on
 hipError_t launch_fp4_zero(uint16_t* y, int64_t n, hipStream_t st);
 hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
-hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st);
+hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, bool exact, hipStream_t st);
 
 }  // namespace fp8lin

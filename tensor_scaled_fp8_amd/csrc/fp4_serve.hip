@@ -262,10 +262,15 @@ inline int part_cols(int64_t N, int most) {
 // and add their sums at the end: where a CU has no other workgroup, its SIMDs
 // then have two waves (222 rows by 7040 x 1664, 104 workgroups: 19.1 us with
 // one group, 14.0 with two; 512 by 12288 x 16384, 512 of them: 96 and 113).
+//
+// EXACT: bf16 products instead, of both codes widened in registers, at half
+// the rate (333 rows by 5120 x 15360: 57 us, 34 of the codes): for a Y that is
+// rounded to 8 bits next. A lane then has elements
+// 32 G ..+31 of X too (of the 8-bit instruction 16 G ..+15 of both halves).
 typedef int f4_v8i __attribute__((ext_vector_type(8)));
 
-template <int MF, int NB, int KG>
-__global__ __launch_bounds__(256 * KG) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_t* __restrict__ y, int tiles_n) {
+template <int MF, int NB, int KG, bool EXACT>
+__global__ __launch_bounds__(256 * KG, EXACT ? 2 : 1) void fp4_many_kernel(Fp4X x, Fp4Mat w, uint16_t* __restrict__ y, int tiles_n) {
   constexpr int kPieces = 2 * MF, kTurns = (kPieces + 3) / 4;  // of 1024 bytes; each wave's
   __shared__ bq_u32x4 xl[KG][2][kPieces][64];
   const int lane = threadIdx.x & 63;
@@ -348,17 +353,39 @@ __global__ __launch_bounds__(256 * KG) void fp4_many_kernel(Fp4X x, Fp4Mat w, ui
           load_scales(kb / 4 + 1);
         }
         constexpr int sel = i * KG % 4;
+        f4_bf16x8 wf[EXACT ? NB : 1][4];
+        if constexpr (EXACT) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t s = wsv[b] >> (8 * sel) & 0xFFu;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wf[b][j] = widen4(wv[i][b][j], s == 255u ? __uint_as_float(0x7FC00000u) : scale_value(s));
+          }
+        }
         load_w(n + 3, wv[(i + 3) & 3]);
         if (kb < nk) {
           // a fragment is read while the one before is multiplied
+          constexpr int second = EXACT ? 16 : 64;
+          const bq_u32x4* const tile = &xl[kg][i & 1][0][0] + (EXACT ? 64 * (G >> 1) + 32 * (G & 1) + r16 : lane);
           bq_u32x4 p[2], q[2];
-          p[0] = xl[kg][i & 1][0][lane];
-          q[0] = xl[kg][i & 1][1][lane];
+          p[0] = tile[0];
+          q[0] = tile[second];
           static_for<MF>([&](auto F_) {
             constexpr int f = decltype(F_)::value, at = f & 1;
             if constexpr (f + 1 < MF) {
-              p[at ^ 1] = xl[kg][i & 1][2 * f + 2][lane];
-              q[at ^ 1] = xl[kg][i & 1][2 * f + 3][lane];
+              p[at ^ 1] = tile[128 * (f + 1)];
+              q[at ^ 1] = tile[128 * (f + 1) + second];
+            }
+            if constexpr (EXACT) {
+              const float s = scale_value(xsv[f] >> (8 * sel) & 0xFFu);
+              const f4_bf16x8 xf[4] = {widen8(p[at].x, p[at].y, s), widen8(p[at].z, p[at].w, s), widen8(q[at].x, q[at].y, s),
+                                       widen8(q[at].z, q[at].w, s)};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc[f][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b][j], xf[j], acc[f][b], 0, 0, 0);
+              __builtin_amdgcn_sched_barrier(0);
+              return;
             }
             const f4_v8i e = {(int)p[at].x, (int)p[at].y, (int)p[at].z, (int)p[at].w,
                               (int)q[at].x, (int)q[at].y, (int)q[at].z, (int)q[at].w};
@@ -418,19 +445,33 @@ __global__ __launch_bounds__(256 * KG) void fp4_many_kernel(Fp4X x, Fp4Mat w, ui
   }
 }
 
-template <int MF, int NB>
+// 16-row fragments of a tile, at most: exact ones hold W's block in bf16 too
+constexpr int most_mf(int nb, bool exact) { return exact && nb == 3 ? 5 : 8; }
+
+template <int MF, int NB, bool EXACT>
 hipError_t run_many(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* y, hipStream_t st) {
   const int64_t tm = ((x.M + 15) / 16 + MF - 1) / MF, tn = (w.N + 64 * NB - 1) / (64 * NB);
-  // (one fragment of columns never goes with more workgroups than CUs: two would take one round less)
-  if (NB == 1 || f.groups == 2) fp4_many_kernel<MF, NB, 2><<<(unsigned)(tm * tn), 512, 0, st>>>(x, w, y, (int)tn);
-  else if constexpr (NB > 1) fp4_many_kernel<MF, NB, 1><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
+  if (NB == 1 || f.groups == 2) fp4_many_kernel<MF, NB, 2, EXACT><<<(unsigned)(tm * tn), 512, 0, st>>>(x, w, y, (int)tn);
+  else if constexpr (NB > 1) fp4_many_kernel<MF, NB, 1, EXACT><<<(unsigned)(tm * tn), 256, 0, st>>>(x, w, y, (int)tn);
   return hipGetLastError();
 }
-template <int MF>
+template <int MF, bool EXACT>
 hipError_t run_rows(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* y, hipStream_t st) {
   if constexpr (MF < 8)
-    if (f.nb == 1) return run_many<MF, 1>(x, w, f, y, st);
-  return f.nb == 2 ? run_many<MF, 2>(x, w, f, y, st) : run_many<MF, 3>(x, w, f, y, st);
+    if (f.nb == 1) return run_many<MF, 1, EXACT>(x, w, f, y, st);
+  if constexpr (MF <= most_mf(3, EXACT))
+    if (f.nb == 3) return run_many<MF, 3, EXACT>(x, w, f, y, st);
+  return run_many<MF, 2, EXACT>(x, w, f, y, st);
+}
+template <bool EXACT>
+hipError_t run_tiles(const Fp4X& x, const Fp4Mat& w, const Fp4Form& f, uint16_t* y, hipStream_t st) {
+  switch (f.mf) {
+    case 4: return run_rows<4, EXACT>(x, w, f, y, st);
+    case 5: return run_rows<5, EXACT>(x, w, f, y, st);
+    case 6: return run_rows<6, EXACT>(x, w, f, y, st);
+    case 7: return run_rows<7, EXACT>(x, w, f, y, st);
+    default: return run_rows<8, EXACT>(x, w, f, y, st);
+  }
 }
 
 __global__ __launch_bounds__(256) void fp4_zero_kernel(uint16_t* __restrict__ y, int64_t n) {
@@ -448,9 +489,10 @@ hipError_t launch_fp4_zero(uint16_t* y, int64_t n, hipStream_t st) {
 // X's values in bf16 fit 64 KB of LDS
 bool fp4_fused(int64_t M, int64_t K) { return M <= 16 && M * fp4_xblocks(K) <= 248; }
 
-Fp4Form fp4_form(int64_t M, int64_t K, int64_t N) {
-  Fp4Form f = {fp4_fused(M, K) ? FP4_FUSED : M <= kFp4Few ? FP4_FEW : FP4_MANY, 1, 1, 1, 0};
-  if (f.kind != FP4_MANY) {
+Fp4Form fp4_form(int64_t M, int64_t K, int64_t N, bool exact) {
+  Fp4Form f = {fp4_fused(M, K) ? FP4_FUSED : M <= (exact ? kFp4FewExact : kFp4Few) ? FP4_FEW : exact ? FP4_EXACT : FP4_MANY,
+               1, 1, 1, 0};
+  if (f.kind == FP4_FUSED || f.kind == FP4_FEW) {
     f.mf = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     f.cols = part_cols(N, 48);
     f.nb = f.cols <= 16 ? 1 : f.cols <= 32 ? 2 : 3;
@@ -461,8 +503,10 @@ Fp4Form fp4_form(int64_t M, int64_t K, int64_t N) {
   int64_t least = 0;
   for (int mf = 4; mf <= 8; ++mf)
     for (int nb = mf == 8 ? 2 : 1; nb <= 3; ++nb) {  // 8 x 1 costs what 4 x 2 does
+      if (mf > most_mf(nb, exact)) continue;
       const int64_t n = (mt + mf - 1) / mf * ((panels + 4 * nb - 1) / (4 * nb));
       // 4 + products: what a block of K costs a wave besides them
+      if (nb == 1 && n > 256) continue;
       const int64_t cost = (n + 255) / 256 * (mf * nb + 4);
       if (least == 0 || cost < least) {
         least = cost;
@@ -478,29 +522,23 @@ Fp4Form fp4_form(int64_t M, int64_t K, int64_t N) {
 hipError_t launch_fp4_fused(const Bf16Mat& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
   if (x.rows == 0 || w.N == 0) return hipSuccess;
   const Fp4X none = {nullptr, nullptr, 0, 0};
-  const Fp4Form f = fp4_form(x.rows, w.K, w.N);
+  const Fp4Form f = fp4_form(x.rows, w.K, w.N, true);
   return f.nb == 1   ? run<true, 1, 1, 4>(x, none, w, y, f.cols, st)
          : f.nb == 2 ? run<true, 1, 2, 4>(x, none, w, y, f.cols, st)
                      : run<true, 1, 3, 4>(x, none, w, y, f.cols, st);
 }
 
-hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, hipStream_t st) {
+hipError_t launch_fp4_linear(const Fp4X& x, const Fp4Mat& w, uint16_t* y, bool exact, hipStream_t st) {
   if (x.M == 0 || w.N == 0) return hipSuccess;
-  const Fp4Form f = fp4_form(x.M, w.K, w.N);
-  if (f.kind != FP4_MANY) {
+  const Fp4Form f = fp4_form(x.M, w.K, w.N, exact);
+  if (f.kind == FP4_FEW) {
     const Bf16Mat none = {nullptr, 0, 0, 0};
 #define FEW(m, n) \
   if (f.mf == m && f.nb == n) return run<false, m, n, (m > 2 ? 2 : 4)>(none, x, w, y, f.cols, st);
     FEW(1, 1) FEW(1, 2) FEW(1, 3) FEW(2, 1) FEW(2, 2) FEW(2, 3) FEW(4, 1) FEW(4, 2) FEW(4, 3)
 #undef FEW
   }
-  switch (f.mf) {
-    case 4: return run_rows<4>(x, w, f, y, st);
-    case 5: return run_rows<5>(x, w, f, y, st);
-    case 6: return run_rows<6>(x, w, f, y, st);
-    case 7: return run_rows<7>(x, w, f, y, st);
-    default: return run_rows<8>(x, w, f, y, st);
-  }
+  return exact ? run_tiles<true>(x, w, f, y, st) : run_tiles<false>(x, w, f, y, st);
 }
 
 }  // namespace fp8lin

@@ -174,10 +174,10 @@ size_t fp4_linear_bytes(int64_t M, int64_t K, int64_t N) {
   return Fp4Scratch(nullptr, M, K).bytes;
 }
 
-fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int* form, int* row_tiles, int* col_tiles, int* groups) {
+fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int exact, int* form, int* row_tiles, int* col_tiles, int* groups) {
   if (M < 0 || !fp4_sizes(K, N) || !form || !row_tiles || !col_tiles || !groups) return FP8_ERR_INVALID;
   if (!fp4_fits(K, N) || !fp4_rows_fit(M, K) || !fp4_product_fits(M, N)) return FP8_ERR_UNSUPPORTED;
-  const Fp4Form f = fp4_form(M, K, N);
+  const Fp4Form f = fp4_form(M, K, N, exact != 0);
   *form = f.kind;
   *row_tiles = f.mf;
   *col_tiles = f.nb;
@@ -186,7 +186,8 @@ fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int* form, int* row_
 }
 
 fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
-                                 const uint8_t* scales, void* scratch, size_t scratch_bytes, void* Y, hipStream_t stream) {
+                                 const uint8_t* scales, int exact, void* scratch, size_t scratch_bytes, void* Y,
+                                 hipStream_t stream) {
   if (M < 0 || !fp4_sizes(K, N) || ldx < 0 || !aligned(X, 2) || !aligned(codes, 16) || !aligned(scales, 16) ||
       !aligned(scratch, 16) || !aligned(Y, 2))
     return FP8_ERR_INVALID;
@@ -201,7 +202,7 @@ fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t 
   const Fp4Scratch s(scratch, M, K);
   const hipError_t e = launch_fp4_x(x, s.x, stream);
   if (e != hipSuccess) return FP8_ERR_HIP;
-  return hip_status(launch_fp4_linear(s.x, w, (uint16_t*)Y, stream));
+  return hip_status(launch_fp4_linear(s.x, w, (uint16_t*)Y, exact != 0, stream));
 }
 
 }  // extern "C"

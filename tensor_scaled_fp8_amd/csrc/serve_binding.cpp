@@ -255,7 +255,7 @@ Tensor fp4_restore(const Tensor& data, int64_t K, int64_t N) {
   return W;
 }
 
-Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, const Maybe& given) {
+Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, const Maybe& given, bool exact) {
   matrix(X, "X");
   if (X.size(1) != K)
     refuse("X " + shape_of(X) + " does not go with the stored weight [" + std::to_string(K) + ", " + std::to_string(N) + "]");
@@ -277,7 +277,7 @@ Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, cons
   const size_t n = api.fp4_linear_bytes(M, K, N);
   Tensor scratch;
   if (n) scratch = at::empty({(int64_t)n}, data.options());
-  check(api.fp4_linear_fwd_cached(ptr(X), X.stride(0), M, K, N, w.codes, w.scales, n ? scratch.data_ptr() : nullptr, n, ptr(Y),
+  check(api.fp4_linear_fwd_cached(ptr(X), X.stride(0), M, K, N, w.codes, w.scales, exact, n ? scratch.data_ptr() : nullptr, n, ptr(Y),
                                   stream_of(X)),
         "fp4_linear_fwd_cached");
   return Y;

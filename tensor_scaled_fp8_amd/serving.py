@@ -155,23 +155,29 @@ def prepare_fp4_weight(W: torch.Tensor) -> FP4Tensor:
     return FP4Tensor(data, *W.shape)
 
 
-def fp4_linear_fwd_cached(X: torch.Tensor, w: FP4Tensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+def fp4_linear_fwd_cached(X: torch.Tensor, w: FP4Tensor, Y: Optional[torch.Tensor] = None,
+                          exact: bool = False) -> torch.Tensor:
     """Y [M, N] = X [M, K] W from a stored 4-bit weight (prepare_fp4_weight);
     X is quantised to E4M3, a scale for each 128 elements of a row. Y, if
-    given, is contiguous and does not overlap X."""
-    return _call(X, "fp4_serve", X, w.data, w.K, w.N, Y)
+    given, is contiguous and does not overlap X. exact: products are exact and
+    sums 32-bit at any number of rows, for a Y that is rounded to 8 bits next;
+    otherwise those of more than 32 rows are as near as fp8_block_gemm's."""
+    return _call(X, "fp4_serve", X, w.data, w.K, w.N, Y, exact)
 
 
 class FP4InferenceLinear(torch.nn.Module):
-    """Forward-only linear on a weight [in, out] stored once in 4 bits."""
+    """Forward-only linear on a weight [in, out] stored once in 4 bits; exact:
+    as of fp4_linear_fwd_cached."""
 
-    def __init__(self, W: torch.Tensor):
+    def __init__(self, W: torch.Tensor, exact: bool = False):
         super().__init__()
+        self.exact = exact
         self.register_buffer("weight", prepare_fp4_weight(W).data)
         self.in_features, self.out_features = W.shape
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y = _call(x, "fp4_serve", _as_rows(x, "x")[0], self.weight, self.in_features, self.out_features, None)
+        y = _call(x, "fp4_serve", _as_rows(x, "x")[0], self.weight, self.in_features, self.out_features, None,
+                  self.exact)
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], self.out_features)
 
 
@@ -195,8 +201,9 @@ class InferenceAttention(torch.nn.Module):
             raise ValueError(f"weights are stored in 4 or 8 bits, got {bits}")
         if freqs is not None and (freqs.dtype is not torch.float32 or freqs.dim() != 1):
             raise ValueError(f"freqs must be float32 and 1-D, got {freqs.dtype} {tuple(freqs.shape)}")
-        linear = FP4InferenceLinear if bits == 4 else BlockInferenceLinear
-        self.qkv, self.out = linear(Wqkv.detach()), linear(Wo.detach())
+        # keys and values go to 8 bits next
+        self.qkv = FP4InferenceLinear(Wqkv.detach(), exact=True) if bits == 4 else BlockInferenceLinear(Wqkv.detach())
+        self.out = (FP4InferenceLinear if bits == 4 else BlockInferenceLinear)(Wo.detach())
         self.register_buffer("freq_bytes", None if freqs is None else freqs.detach().contiguous().view(_U8))
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.interleaved, self.scale, self.softcap, self.window = interleaved, scale, softcap, window

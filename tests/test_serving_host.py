@@ -128,20 +128,20 @@ def test_attention_forms():
 
 def test_fp4_forms():
     """The sizes that the GPU tests take reach every form that any size up to 700 rows chooses."""
-    from tests.test_gpu_fp4 import FORMS, blocks_of
+    from tests.test_gpu_fp4 import FORMS, blocks_of, is_exact
 
-    def fp4_plan(M, K, N):
+    def fp4_plan(M, K, N, exact):
         v = [ctypes.c_int() for _ in range(4)]
-        assert tsf.load().fp4_linear_plan(M, K, N, *map(ctypes.byref, v)) == 0
+        assert tsf.load().fp4_linear_plan(M, K, N, exact, *map(ctypes.byref, v)) == 0
         return tuple(x.value for x in v)
     for form, (M, N) in FORMS.items():
-        assert fp4_plan(M, blocks_of(form), N) == form
-    seen = {fp4_plan(M, K, N) for M in (1, 2, 16, 17, 32, 33, 64, *range(65, 700, 13)) for K in (200, 4000)
+        assert fp4_plan(M, blocks_of(form), N, is_exact(form)) == form
+    seen = {fp4_plan(M, K, N, e) for M in (1, 2, 16, 17, 32, 33, 64, *range(65, 700, 13)) for K in (200, 4000) for e in (0, 1)
             for N in (1, 17, 300, 4096, 4097, 8193, *range(9000, 40000, 700))}
     assert seen <= set(FORMS), seen - set(FORMS)
-    assert tsf.load().fp4_linear_plan(-1, 1, 1, *[ctypes.byref(ctypes.c_int())] * 4) == INV
-    assert tsf.load().fp4_linear_plan(1 << 40, 1, 1, *[ctypes.byref(ctypes.c_int())] * 4) == UNS
-    assert tsf.load().fp4_linear_plan(1, 1, 1, None, None, None, None) == INV
+    assert tsf.load().fp4_linear_plan(-1, 1, 1, 0, *[ctypes.byref(ctypes.c_int())] * 4) == INV
+    assert tsf.load().fp4_linear_plan(1 << 40, 1, 1, 0, *[ctypes.byref(ctypes.c_int())] * 4) == UNS
+    assert tsf.load().fp4_linear_plan(1, 1, 1, 0, None, None, None, None) == INV
 
 
 def test_fp4_arguments_without_launch():
@@ -154,7 +154,7 @@ def test_fp4_arguments_without_launch():
             assert g(*args(**change), None) == INV, change
         assert g(*args(K=(1 << 20) + 1), None) == UNS
     assert d(OK, OK, 32, 16, OK, 8, None) == INV
-    ok = dict(X=OK, ldx=32, M=20, K=32, N=16, c=OK, s=OK, ws=OK, n=1 << 30, Y=OK)
+    ok = dict(X=OK, ldx=32, M=20, K=32, N=16, c=OK, s=OK, exact=0, ws=OK, n=1 << 30, Y=OK)
     for change in (dict(X=None), dict(X=OK + 1), dict(M=-1), dict(ldx=-1), dict(c=None), dict(s=OK + 8), dict(ws=None),
                    dict(ws=OK + 8), dict(n=0), dict(Y=None)):
         assert f(*{**ok, **change}.values(), None) == INV, change
