@@ -22,8 +22,8 @@
 // call that waits for the cache's bytes does not notice.
 //
 // Few rows (a decode batch): the work of all (sequence, tile, head) is one
-// line of units of 128 tokens, cut into equal shares, one a workgroup, as
-// many as the chip holds at once: whatever the lengths, all CUs end together.
+// line of units of 128 tokens, cut into equal shares, one a workgroup, two or
+// three a CU: whatever the lengths, all CUs end together.
 // A tile cut by a share's end leaves its parts' sums in the workspace, and a
 // second launch joins them. Many rows (prompts): one workgroup a tile, the
 // longest first; of still more, one wave a tile.
