@@ -22,7 +22,9 @@ CASES = [
     (TILES, 128, 128, 64, [130, 64, 97, 300], [130, 64, 97, 200]), (TILES, 64, 192, 128, [140, 250, 60], [140, 250, 60]),
     (TILES, 64, 128, 256, [140, 77, 210], [140, 77, 200]),
     (ROWS, 128, 512, 64, [300, 171, 65], [300, 171, 65]), (ROWS, 64, 512, 128, [200, 120, 97, 31], [200, 120, 97, 31]),
-    (ROWS, 64, 256, 256, [150, 99, 190], [150, 99, 100])]
+    (ROWS, 64, 256, 256, [150, 99, 190], [150, 99, 100]),
+    # 256 tiles and more: three workgroups a CU share them
+    (SHARES, 64, 128, 64, [600, 70, 5, 33, 1000], [2, 2, 2, 2, 2]), (SHARES, 40, 80, 128, [700, 33, 5, 1, 90, 300, 64], [1] * 7)]
 
 
 def reference(q, k, v, pos, there, softcap, window):
