@@ -7,6 +7,13 @@
  * memory, errors are status codes, work goes to the caller's stream of the
  * current device, nothing is allocated and nothing waits. Calls with equal
  * arguments give equal bits.
+ *
+ * An output is read or written by others of the same launch in no order, so
+ * it may share memory with an input only where this is said below, and then
+ * has to be that input, row for row: packed rows that overlap otherwise (an
+ * output's own, too) are FP8_ERR_INVALID. Views of one tensor with the same
+ * strides are told apart element by element, others by whether their tokens
+ * lie beside each other.
  */
 #ifndef FP8LIN_SERVE_H
 #define FP8LIN_SERVE_H
@@ -84,7 +91,7 @@ size_t fp8_cache_scales_bytes(int64_t pages, int page_tokens, int heads, int hea
  * Angles, and keys up to their codes, are computed in 64 bits (sin and cos
  * at far positions; codes are the nearest to the rotated key itself).
  * Queries, if q.p is not NULL, go rotated to q_out (any strides; it may be
- * q itself), rounded to bf16, of q_heads heads; with rot = 0 they are copied.
+ * q itself, and overlap no other input), rounded to bf16, of q_heads heads; with rot = 0 they are copied.
  * Scales: for a block's new tokens, over its finite values,
  *   need = floor(log2(448 / max |x|)), clamped to [-126, 126]; 126 if all
  *          are 0; at most 0 if one is infinite;
@@ -102,7 +109,7 @@ fp8_status fp8_cache_append(const fp8_cache* cache, const fp8_cache_batch* batch
                             const float* freqs, int rot, int interleaved, hipStream_t stream);
 
 /* The values of the batch's tokens as the cache holds them, to bf16 (exact
- * within its normal range). */
+ * within its normal range). k and v may not overlap. */
 fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, const fp8_cache_rows* k,
                           const fp8_cache_rows* v, hipStream_t stream);
 
@@ -167,7 +174,7 @@ fp8_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t K
  * are exact and their sums 32-bit, for a Y that is rounded to 8 bits next.
  * Without it products of more than 32 rows are fp8_block_gemm's, up to twice
  * as fast and 1.5e-5 off, which a bf16 Y does not show; of fewer they are
- * exact all the same. scratch: fp4_linear_bytes (0: none is needed).
+ * exact all the same. Y does not overlap X. scratch: fp4_linear_bytes (0: none is needed).
  */
 /* How a product is cut: the kernel, its wave's 16-row and 16-column tiles and
  * the groups of waves that share K. For profiles and tests. */

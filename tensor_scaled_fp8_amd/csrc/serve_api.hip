@@ -2,6 +2,7 @@
 // launches on the caller's stream. No allocation, no host synchronisation.
 #include "cache.h"
 #include "fp4.h"
+#include "serve_overlap.h"
 
 using namespace fp8lin;
 
@@ -39,6 +40,13 @@ CacheBatch batch_of(const fp8_cache_batch* b) {
   return {b->tables, b->ld_tables, b->table_pages, b->lengths, b->starts, (int)b->sequences, (int)b->tokens};
 }
 CacheRows rows_of(const fp8_cache_rows* r) { return {(uint16_t*)r->p, r->token_stride, r->head_stride}; }
+RowSet set_of(const fp8_cache_rows* r, int64_t tokens, int heads, int head_dim) {
+  return {r->p, tokens, heads, head_dim, r->token_stride, r->head_stride};
+}
+// out is written while in is read: it is in itself or lies apart, and its own rows do
+inline bool rows_apart(const RowSet& out, const RowSet& in) {
+  return !overlaps_itself(out) && (same_rows(out, in) || !overlap(out, in));
+}
 inline bool q_heads_ok(int q_heads, int heads) { return q_heads > 0 && q_heads <= 16384 && q_heads % heads == 0; }
 
 CacheAttend attend_of(const fp8_cache* c, const fp8_cache_batch* b, int q_heads) {
@@ -93,6 +101,13 @@ fp8_status fp8_cache_append(const fp8_cache* cache, const fp8_cache_batch* batch
     return FP8_ERR_INVALID;
   if (rot < 0 || rot % 16 || rot > cache->head_dim || (rot && (!freqs || !aligned(freqs, 4)))) return FP8_ERR_INVALID;
   if (!batch_fits(batch)) return FP8_ERR_UNSUPPORTED;
+  if (with_q) {
+    const RowSet out = set_of(q_out, batch->tokens, q_heads, cache->head_dim);
+    if (!rows_apart(out, set_of(q, batch->tokens, q_heads, cache->head_dim)) ||
+        overlap(out, set_of(k, batch->tokens, cache->heads, cache->head_dim)) ||
+        overlap(out, set_of(v, batch->tokens, cache->heads, cache->head_dim)))
+      return FP8_ERR_INVALID;
+  }
   CacheAppend a = {cache_of(cache), batch_of(batch), rows_of(k), rows_of(v), {nullptr, 0, 0}, {nullptr, 0, 0}, 0, rot,
                    interleaved != 0, freqs};
   if (with_q) {
@@ -108,6 +123,9 @@ fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, 
   if (!cache_ok(cache) || !batch_ok(batch) || !rows_ok(k, batch->tokens) || !rows_ok(v, batch->tokens))
     return FP8_ERR_INVALID;
   if (!batch_fits(batch)) return FP8_ERR_UNSUPPORTED;
+  const RowSet rk = set_of(k, batch->tokens, cache->heads, cache->head_dim);
+  const RowSet rv = set_of(v, batch->tokens, cache->heads, cache->head_dim);
+  if (overlaps_itself(rk) || overlaps_itself(rv) || overlap(rk, rv)) return FP8_ERR_INVALID;
   return hip_status(launch_cache_read(cache_of(cache), batch_of(batch), rows_of(k), rows_of(v), cache->head_dim, stream));
 }
 
@@ -135,6 +153,8 @@ fp8_status fp8_cache_attention(const fp8_cache* cache, const fp8_cache_batch* ba
       !(__builtin_fabsf(scale) <= 0x1p64f) || !aligned(lse, 4) || !aligned(ws, 16))
     return FP8_ERR_INVALID;
   if (!attend_fits(batch, q_heads)) return FP8_ERR_UNSUPPORTED;
+  if (!rows_apart(set_of(out, batch->tokens, q_heads, cache->head_dim), set_of(q, batch->tokens, q_heads, cache->head_dim)))
+    return FP8_ERR_INVALID;
   CacheAttend a = attend_of(cache, batch, q_heads);
   a.q = rows_of(q);
   a.out = rows_of(out);
@@ -193,6 +213,9 @@ fp8_status fp4_linear_fwd_cached(const void* X, int64_t ldx, int64_t M, int64_t 
     return FP8_ERR_INVALID;
   if ((M && K && !X) || (K && N && (!codes || !scales)) || (M && N && !Y)) return FP8_ERR_INVALID;
   if (!fp4_fits(K, N) || !fp4_rows_fit(M, K) || !fp4_product_fits(M, N)) return FP8_ERR_UNSUPPORTED;
+  // X is read until the last workgroup ends
+  const RowSet xs(X, M, 1, K, ldx, 0), ys(Y, M, 1, N, N, 0);
+  if (!xs.empty() && !ys.empty() && xs.lo() < ys.hi() && ys.lo() < xs.hi()) return FP8_ERR_INVALID;
   const size_t need = fp4_linear_bytes(M, K, N);
   if (need && (!scratch || scratch_bytes < need)) return FP8_ERR_INVALID;
   const Bf16Mat x = {(const uint16_t*)X, ldx, M, K};

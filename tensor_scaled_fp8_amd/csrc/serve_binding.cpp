@@ -10,6 +10,7 @@
 #include <optional>
 
 #include "fp8lin_serve.h"
+#include "serve_overlap.h"
 
 namespace {
 
@@ -116,6 +117,19 @@ fp8_cache_rows rows_of(const Tensor& t, int64_t tokens, int64_t heads, int64_t h
     refuse(std::string(name) + " must not be expanded: it is written");
   return {ptr(t), t.stride(0), t.stride(1)};
 }
+fp8lin::RowSet set_of(const Tensor& t) {
+  return {ptr(t), t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1)};
+}
+// An output that the caller gives, against an input of the same call
+void apart(const Tensor& out, const char* name, const Tensor& in, const char* other, bool or_itself) {
+  const fp8lin::RowSet a = set_of(out), b = set_of(in);
+  if (or_itself && fp8lin::same_rows(a, b)) return;
+  if (fp8lin::overlap(a, b))
+    refuse(std::string(name) + " must " + (or_itself ? std::string("be ") + other + " itself or " : "") + "not overlap " + other);
+}
+void apart(const Tensor& out, const char* name) {
+  if (fp8lin::overlaps_itself(set_of(out))) refuse(std::string(name) + " must not overlap itself: it is written");
+}
 void q_heads_of(const Tensor& q, int64_t heads) {
   if (q.dim() == 3 && (q.size(1) == 0 || q.size(1) % heads))
     refuse("q has " + std::to_string(q.size(1)) + " heads: not a multiple of the cache's " + std::to_string(heads));
@@ -143,7 +157,13 @@ Maybe append(const Tensor& data, int64_t pages, int64_t page_tokens, int64_t hea
     rq = rows_of(*q, tokens, -1, head_dim, "q", false);
     q_heads_of(*q, heads);
     q_heads = (int)q->size(1);
-    if (q_out) ro = rows_of(*q_out, tokens, q_heads, head_dim, "q_out", true);
+    if (q_out) {
+      ro = rows_of(*q_out, tokens, q_heads, head_dim, "q_out", true);
+      apart(*q_out, "q_out");
+      apart(*q_out, "q_out", *q, "q", true);
+      apart(*q_out, "q_out", k, "k", false);
+      apart(*q_out, "q_out", v, "v", false);
+    }
   }
   no_grad(k, "k");
   no_grad(v, "v");
@@ -173,8 +193,15 @@ std::pair<Tensor, Tensor> read_back(const Tensor& data, int64_t pages, int64_t p
   const fp8_cache c = cache_of(data, pages, page_tokens, heads, head_dim);
   if (tokens < 0) refuse("tokens must not be negative");
   const fp8_cache_batch b = batch_of(tables, lengths, starts, tokens);
-  if (k) rows_of(*k, tokens, heads, head_dim, "k", true);
-  if (v) rows_of(*v, tokens, heads, head_dim, "v", true);
+  if (k) {
+    rows_of(*k, tokens, heads, head_dim, "k", true);
+    apart(*k, "k");
+  }
+  if (v) {
+    rows_of(*v, tokens, heads, head_dim, "v", true);
+    apart(*v, "v");
+  }
+  if (k && v) apart(*k, "k", *v, "v", false);
   on_device(data, "cache");
   batch_on(tables, lengths, starts, data);
   if (k) on(*k, data, "k");
@@ -196,7 +223,11 @@ std::pair<Tensor, Maybe> attention(const Tensor& data, int64_t pages, int64_t pa
   q_heads_of(q, heads);
   const int64_t q_heads = q.size(1);
   const fp8_cache_batch b = batch_of(tables, lengths, starts, tokens);
-  if (given) rows_of(*given, tokens, q_heads, head_dim, "out", true);
+  if (given) {
+    rows_of(*given, tokens, q_heads, head_dim, "out", true);
+    apart(*given, "out");
+    apart(*given, "out", q, "q", true);
+  }
   if (!(softcap == 0 || (softcap >= 0x1p-64 && softcap <= 0x1p64))) refuse("softcap must be 0 or between 2^-64 and 2^64");
   if (!(std::fabs(scale) <= 0x1p64)) refuse("scale must be finite, up to 2^64");
   if (window < 0 || window > INT32_MAX) refuse("window must be between 0 and 2^31 - 1");

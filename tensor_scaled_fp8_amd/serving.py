@@ -80,8 +80,8 @@ def fp8_cache_append(cache: BlockKVCache, k: torch.Tensor, v: torch.Tensor, tabl
     With freqs (float32, half as many as the rotated dimensions, a multiple of
     16 from the first on) k and q are rotated by position * freqs: pairs
     (j, j + half), or neighbours if interleaved. Returns q [tokens, any
-    multiple of heads, head_dim] rotated, in q_out (which may be q) if given;
-    None without q. Keys are rotated in 64 bits and rounded once. A block's
+    multiple of heads, head_dim] rotated, in q_out if given (which may be q
+    itself and may not overlap q, k or v otherwise); None without q. Keys are rotated in 64 bits and rounded once. A block's
     scale follows its largest token; earlier tokens of it are rounded anew
     when it grows. A page that two sequences share must not be appended to."""
     return _call(cache.data, "cache_append", *cache._of(), k, v, tables, lengths, starts, q, freqs, interleaved,
@@ -93,7 +93,8 @@ def fp8_cache_read(cache: BlockKVCache, tables: torch.Tensor, lengths: torch.Ten
                    v: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The sequences' last tokens (starts of `tokens` rows in all; without, one
     each) as the cache holds them: keys and values, bf16 [tokens, heads,
-    head_dim], in k and v if given; zeros where there is no page."""
+    head_dim], in k and v (which may not overlap) if given; zeros where there
+    is no page."""
     if tokens is None:
         if starts is not None:
             raise ValueError("tokens (the rows of all sequences) must be given with starts")
@@ -108,8 +109,9 @@ def fp8_cache_attention(q: torch.Tensor, cache: BlockKVCache, tables: torch.Tens
     which holds these tokens' own keys and values already. The query at
     position p sees positions j <= p, and j > p - window if window > 0. Scores
     are scale (default head_dim^-0.5) q . k, then softcap tanh(score / softcap)
-    if softcap > 0. Returns [tokens, heads of q, head_dim] (in out, which may be
-    q, if given), 0 where nothing is seen; with lse also the logarithms of the sums, float32 [tokens, heads of
+    if softcap > 0. Returns [tokens, heads of q, head_dim] (in out, if given,
+    which may be q itself and may not overlap it otherwise), 0 where nothing is
+    seen; with lse also the logarithms of the sums, float32 [tokens, heads of
     q], -inf there."""
     if scale is None:
         scale = cache.head_dim ** -0.5
