@@ -60,6 +60,10 @@ void no_grad(const Tensor& t, const char* name) {
     throw py::error_already_set();
   }
 }
+// A tensor that a call wrote: a backward that saved it finds out by its version
+void wrote(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 void on(const Tensor& t, const Tensor& like, const char* name) {
   if (t.device() != like.device()) refuse(std::string(name) + " must be on " + like.device().str() + ", got " + t.device().str());
 }
@@ -169,6 +173,7 @@ Maybe append(const Tensor& data, int64_t pages, int64_t page_tokens, int64_t hea
   no_grad(v, "v");
   if (q) no_grad(*q, "q");
   if (freqs) no_grad(*freqs, "freqs");
+  if (q_out) no_grad(*q_out, "q_out");
   on_device(data, "cache");
   on(k, data, "k");
   on(v, data, "v");
@@ -184,6 +189,8 @@ Maybe append(const Tensor& data, int64_t pages, int64_t page_tokens, int64_t hea
   check(api.fp8_cache_append(&c, &b, &rk, &rv, &rq, &ro, q_heads, freqs ? (const float*)ptr(*freqs) : nullptr, rot, interleaved,
                              stream_of(data)),
         "fp8_cache_append");
+  wrote(data);
+  if (q_out) wrote(*q_out);
   return out;
 }
 
@@ -202,6 +209,8 @@ std::pair<Tensor, Tensor> read_back(const Tensor& data, int64_t pages, int64_t p
     apart(*v, "v");
   }
   if (k && v) apart(*k, "k", *v, "v", false);
+  if (k) no_grad(*k, "k");
+  if (v) no_grad(*v, "v");
   on_device(data, "cache");
   batch_on(tables, lengths, starts, data);
   if (k) on(*k, data, "k");
@@ -211,6 +220,8 @@ std::pair<Tensor, Tensor> read_back(const Tensor& data, int64_t pages, int64_t p
   const Tensor vo = v ? *v : at::empty({tokens, heads, head_dim}, options);
   const fp8_cache_rows rk = {ptr(ko), ko.stride(0), ko.stride(1)}, rv = {ptr(vo), vo.stride(0), vo.stride(1)};
   check(api.fp8_cache_read(&c, &b, &rk, &rv, stream_of(data)), "fp8_cache_read");
+  if (k) wrote(*k);
+  if (v) wrote(*v);
   return {ko, vo};
 }
 
@@ -232,6 +243,7 @@ std::pair<Tensor, Maybe> attention(const Tensor& data, int64_t pages, int64_t pa
   if (!(std::fabs(scale) <= 0x1p64)) refuse("scale must be finite, up to 2^64");
   if (window < 0 || window > INT32_MAX) refuse("window must be between 0 and 2^31 - 1");
   no_grad(q, "q");
+  if (given) no_grad(*given, "out");
   on_device(data, "cache");
   on(q, data, "q");
   batch_on(tables, lengths, starts, data);
@@ -246,6 +258,7 @@ std::pair<Tensor, Maybe> attention(const Tensor& data, int64_t pages, int64_t pa
   check(api.fp8_cache_attention(&c, &b, &rq, (int)q_heads, (float)scale, (float)softcap, (int)window, &ro,
                                 lse ? (float*)ptr(*lse) : nullptr, n ? ws.data_ptr() : nullptr, n, stream_of(data)),
         "fp8_cache_attention");
+  if (given) wrote(*given);
   return {out, lse};
 }
 
@@ -301,6 +314,7 @@ Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, cons
     if (x0 && y0 && x0 < y0 + 2 * M * N && y0 < x0 + 2 * ((M - 1) * X.stride(0) + K)) refuse("Y must not overlap X");
   }
   no_grad(X, "X");
+  if (given) no_grad(*given, "Y");
   on_device(X, "X");
   on(data, X, "w");
   if (given) on(*given, X, "Y");
@@ -311,6 +325,7 @@ Tensor fp4_serve(const Tensor& X, const Tensor& data, int64_t K, int64_t N, cons
   check(api.fp4_linear_fwd_cached(ptr(X), X.stride(0), M, K, N, w.codes, w.scales, exact, n ? scratch.data_ptr() : nullptr, n, ptr(Y),
                                   stream_of(X)),
         "fp4_linear_fwd_cached");
+  if (given) wrote(*given);
   return Y;
 }
 

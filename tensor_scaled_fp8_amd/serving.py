@@ -21,7 +21,8 @@ sequence is one of length 0; rows behind the last sequence are left alone.
 
 Tensors are bf16 on the device, [tokens, heads, head_dim] of any strides with
 a contiguous last dimension. There are no derivatives: tensors that want a
-gradient are refused. Work runs on the current stream of the cache's device."""
+gradient, outputs among them, are refused, and an output that is given counts
+as changed in place. Work runs on the current stream of the cache's device."""
 from __future__ import annotations
 
 from typing import Optional, Tuple

@@ -143,3 +143,19 @@ def test_library_refuses_them():
     for other in (0, 64, 128 * 2):
         assert lib.fp8_cache_read(r(c), r(b), r(row(0, 128)), r(row(other, 128)), None) == INV
     assert lib.fp4_linear_fwd_cached(at, 32, 20, 32, 16, at, at, 0, at, 1 << 30, at + 4, None) == INV
+
+
+def test_outputs_that_want_a_gradient():
+    def made(*shape):
+        return z(*shape).requires_grad_()
+    w = tsf.FP4Tensor(torch.zeros(4352, dtype=torch.uint8), 512, 16)
+    calls = {"q_out": lambda: append(q_out=made(T, 4, D)), "out": lambda: attention(out=made(T, 4, D)),
+             "k": lambda: read(made(T, 2, D), None), "v": lambda: read(None, made(T, 2, D)),
+             "Y": lambda: tsf.fp4_linear_fwd_cached(z(2, 512), w, made(2, 16))}
+    for name, call in calls.items():
+        with pytest.raises(NotImplementedError, match=f"^{name} wants a gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
+            call()
+    with torch.autograd.forward_ad.dual_level(), pytest.raises(NotImplementedError, match="out wants a gradient"):
+        attention(out=torch.autograd.forward_ad.make_dual(z(T, 4, D), z(T, 4, D)))
