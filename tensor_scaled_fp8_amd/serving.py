@@ -28,6 +28,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import _at
 from .block import BlockInferenceLinear, _as_rows, _binding, _wants_grad
@@ -40,6 +41,13 @@ def _call(t: torch.Tensor, entry: str, *args):
     """A function of the compiled binding with t's device current; it refuses tensors that are on none."""
     f = getattr(_binding(), entry)
     return _at(t, f, *args) if t.is_cuda else f(*args)
+
+
+def _no_tangent(**tensors):
+    """What is stored once is a constant from then on: a parameter may be, a tangent would be left behind."""
+    for name, t in tensors.items():
+        if forward_ad._current_level >= 0 and t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} wants a gradient: the serving operators have none (its tangent would be lost)")
 
 
 class BlockKVCache:
@@ -154,6 +162,7 @@ class FP4Tensor:
 
 def prepare_fp4_weight(W: torch.Tensor) -> FP4Tensor:
     """A bf16 weight W [K, N] stored once for inference in 4 bits."""
+    _no_tangent(W=W)
     data = _call(W, "fp4_store", W.detach())
     return FP4Tensor(data, *W.shape)
 
@@ -204,6 +213,7 @@ class InferenceAttention(torch.nn.Module):
             raise ValueError(f"weights are stored in 4 or 8 bits, got {bits}")
         if freqs is not None and (freqs.dtype is not torch.float32 or freqs.dim() != 1):
             raise ValueError(f"freqs must be float32 and 1-D, got {freqs.dtype} {tuple(freqs.shape)}")
+        _no_tangent(Wqkv=Wqkv, Wo=Wo, freqs=freqs)
         # keys and values go to 8 bits next
         self.qkv = FP4InferenceLinear(Wqkv.detach(), exact=True) if bits == 4 else BlockInferenceLinear(Wqkv.detach())
         self.out = (FP4InferenceLinear if bits == 4 else BlockInferenceLinear)(Wo.detach())

@@ -1,6 +1,6 @@
-"""Outputs that a caller gives to the serving operators, without a GPU: those
-that overlap an input, each other or themselves are refused before anything
-is launched, by the binding and by the library."""
+"""Arguments of the serving operators, without a GPU: outputs that overlap an
+input, each other or themselves are refused before anything is launched, by
+the binding and by the library, and so is what would lose a gradient."""
 import ctypes
 import random
 
@@ -159,3 +159,22 @@ def test_outputs_that_want_a_gradient():
             call()
     with torch.autograd.forward_ad.dual_level(), pytest.raises(NotImplementedError, match="out wants a gradient"):
         attention(out=torch.autograd.forward_ad.make_dual(z(T, 4, D), z(T, 4, D)))
+
+
+def test_weights_that_carry_a_tangent():
+    """Stored ones are constants: a parameter may be, a tangent would be lost."""
+    with torch.autograd.forward_ad.dual_level():
+        def dual(*shape, dtype=torch.bfloat16):
+            return torch.autograd.forward_ad.make_dual(z(*shape, dtype=dtype), z(*shape, dtype=dtype))
+        for make in (tsf.prepare_fp4_weight, tsf.FP4InferenceLinear):
+            with pytest.raises(NotImplementedError, match="W wants a gradient"):
+                make(dual(8, 16))
+            with pytest.raises(ValueError, match="device tensor"):
+                make(torch.nn.Parameter(z(8, 16)))
+        sizes = {"Wqkv": (8, 4 * D), "Wo": (2 * D, 8), "freqs": (D // 2,)}
+        for name in sizes:
+            for bits in (4, 8):
+                w = {n: (dual if n == name else z)(*s, dtype=torch.float32 if n == "freqs" else torch.bfloat16)
+                     for n, s in sizes.items()}
+                with pytest.raises(NotImplementedError, match=f"{name} wants a gradient"):
+                    tsf.InferenceAttention(w["Wqkv"], w["Wo"], 2, 1, D, freqs=w["freqs"], bits=bits)
