@@ -182,11 +182,12 @@ __device__ inline void load_codes(const CacheAttend& a, const Blocks& bl, int n,
 }
 // How a product of a query and a key becomes a weight's exponent: times unit,
 // after tanh with a cap. A negative scale's sign goes to the queries, and of a
-// scale of 0 they are 0, so that unit is above 0 and the largest score is the
-// largest product's.
+// scale of 0 they are 0 (NaN where they are not finite, as 0 times them is), so
+// that unit is above 0 and the largest score is the largest product's.
 struct Scores {
   float unit, per_cap, cap_log2, twice;  // twice: 2 log2(e) per_cap, or 0 for a cap above kNearCap
-  uint32_t flip, keep;  // of the queries' bits
+  uint32_t flip;  // of the queries' bits
+  bool none;      // scale 0
 };
 // Up to this cap 1 - 2 / (exp(2 x) + 1) is near enough for tanh near 0 too:
 // 3 2^-24 off, of a score 2^-16, a weight's own rounding. It takes 3
@@ -197,7 +198,7 @@ __device__ inline Scores scores_of(const CacheAttend& a, bool cap) {
   const float scale = a.scale == 0 ? 1.0f : __builtin_fabsf(a.scale);
   const float per_cap = cap ? __builtin_fminf(scale / a.cap, 0x1p120f) : 0.0f;
   return {cap ? 1.0f : scale * kLog2e, per_cap, cap ? a.cap * kLog2e : 0.0f, a.cap <= kNearCap ? 2.0f * kLog2e * per_cap : 0.0f,
-          a.scale < 0 ? 0x80008000u : 0u, a.scale == 0 ? 0u : 0xFFFFFFFFu};
+          a.scale < 0 ? 0x80008000u : 0u, a.scale == 0};
 }
 
 // Step n's scales
@@ -423,13 +424,18 @@ struct LdsQueries {
   __device__ ca_bf16x8 get(int r, int i) const { return __builtin_bit_cast(ca_bf16x8, q[(r * (D / 32) + i) * 64 + lane]); }
 };
 
+// 0 times two bf16
+__device__ inline uint32_t times_zero(uint32_t w) {
+  return ((w & 0x7F80u) == 0x7F80u ? 0x7FC0u : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : 0u);
+}
 template <int D>
 __device__ inline ca_u32x4 query_at(const CacheAttend& a, const Scores& sc, const Tile& t, int row, int i, int g) {
   if (row >= t.s.n * a.group) return (ca_u32x4){0, 0, 0, 0};
   const int tok = row / a.group, head = t.h * a.group + row % a.group;
   const ca_u32x4 w = *(const bq_u32x4_a2*)(a.q.p + (int64_t)(t.s.row0 + tok) * a.q.tok + head * a.q.head + 64 * (i / 2) +
                                            16 * g + 8 * (i % 2));
-  return (w ^ sc.flip) & sc.keep;
+  if (sc.none) return (ca_u32x4){times_zero(w.x), times_zero(w.y), times_zero(w.z), times_zero(w.w)};
+  return w ^ sc.flip;
 }
 
 // The waves' sums (their maxima and sums are in sh.ml already) joined and written
