@@ -213,6 +213,19 @@ class InferenceAttention(torch.nn.Module):
             raise ValueError(f"weights are stored in 4 or 8 bits, got {bits}")
         if freqs is not None and (freqs.dtype is not torch.float32 or freqs.dim() != 1):
             raise ValueError(f"freqs must be float32 and 1-D, got {freqs.dtype} {tuple(freqs.shape)}")
+        # what the attention would refuse after the tokens are appended
+        if kv_heads <= 0 or heads <= 0 or heads % kv_heads or head_dim not in (64, 128, 256):
+            raise ValueError(f"{heads} and {kv_heads} heads of {head_dim}: query heads are a multiple of the key heads, a head "
+                             "has 64, 128 or 256 elements")
+        if freqs is not None and (freqs.numel() % 8 or 2 * freqs.numel() > head_dim):
+            raise ValueError(f"freqs must be half as many as the rotated dimensions, a multiple of 16 up to {head_dim}, got "
+                             f"{freqs.numel()}")
+        if scale is not None and not abs(scale) <= 2.0 ** 64:
+            raise ValueError("scale must be finite, up to 2^64")
+        if not (softcap == 0 or 2.0 ** -64 <= softcap <= 2.0 ** 64):
+            raise ValueError("softcap must be 0 or between 2^-64 and 2^64")
+        if not 0 <= window < 2 ** 31:
+            raise ValueError("window must be between 0 and 2^31 - 1")
         _no_tangent(Wqkv=Wqkv, Wo=Wo, freqs=freqs)
         # keys and values go to 8 bits next
         self.qkv = FP4InferenceLinear(Wqkv.detach(), exact=True) if bits == 4 else BlockInferenceLinear(Wqkv.detach())

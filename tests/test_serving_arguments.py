@@ -178,3 +178,21 @@ def test_weights_that_carry_a_tangent():
                      for n, s in sizes.items()}
                 with pytest.raises(NotImplementedError, match=f"{name} wants a gradient"):
                     tsf.InferenceAttention(w["Wqkv"], w["Wo"], 2, 1, D, freqs=w["freqs"], bits=bits)
+
+
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("change,said", [
+    (dict(scale=NAN), "scale must be"), (dict(scale=-1e20), "scale must be"), (dict(softcap=-1.0), "softcap must be"),
+    (dict(softcap=NAN), "softcap must be"), (dict(softcap=1e20), "softcap must be"), (dict(window=-1), "window must be"),
+    (dict(window=2 ** 31), "window must be"), (dict(heads=3, kv=2), "multiple of the key heads"),
+    (dict(heads=2, kv=0), "multiple of the key heads"), (dict(d=80), "64, 128 or 256"), (dict(freqs=torch.zeros(20)), "multiple of 16"),
+    (dict(freqs=torch.zeros(40)), "multiple of 16"), ({}, "device tensor"), (dict(softcap=30.0, window=5, scale=-0.1), "device tensor")])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_layers_that_are_refused(bits, change, said):
+    """When they are made, and not after their first call's tokens are in the cache."""
+    how = dict(change)
+    heads, kv, d = how.pop("heads", 2), how.pop("kv", 1), how.pop("d", D)
+    with pytest.raises(ValueError, match=said):
+        tsf.InferenceAttention(z(8, (heads + 2 * kv) * d), z(heads * d, 8), heads, kv, d, bits=bits, **how)
