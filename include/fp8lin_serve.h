@@ -127,7 +127,8 @@ fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, 
  * is bf16 (any strides), lse fp32 [tokens, q_heads] or NULL. Weights enter as
  * two bf16 each, 2^-17 off, so that out is as far off as its own rounding;
  * of prompts large enough to wait for the products and not for memory
- * (FP8_CACHE_TILES and _ROWS) as one, 2^-9 off. A NaN in a key or value
+ * (FP8_CACHE_TILES and _ROWS) as one, 2^-9 off; lse is the 32-bit weights'
+ * in every form. A NaN in a key or value
  * reaches the queries that see it and no others.
  *   ws: fp8_cache_attention_workspace_bytes of the same cache and batch
  *   (their sizes alone count), 16-B aligned; it holds nothing between calls.

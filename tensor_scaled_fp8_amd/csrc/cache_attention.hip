@@ -19,7 +19,12 @@
 // FINE: a weight goes into the product as two bf16, its rounding and what
 // that left (2^-17 of it): the outputs are then bf16's own rounding off and no
 // more. It costs a second product of V and a third of the softmax, which a
-// call that waits for the cache's bytes does not notice.
+// call that waits for the cache's bytes does not notice. Otherwise outputs are
+// divided by the sum of the rounded weights, and LSE keeps the sum of the
+// weights themselves beside it, for the logarithm alone: prompts of 31 to 250
+// tokens 1.1e-6 off, by the sum of the rounded ones, 2^-9 off each, 0.0029. A
+// call that asks for it pays with its VALU (prompts of 1501 to 6007 tokens:
+// 704 us without, 770).
 //
 // Few rows (a decode batch): the work of all (sequence, tile, head) is one
 // line of units of 128 tokens, cut into equal shares, one a workgroup, two or
@@ -143,6 +148,7 @@ __device__ inline Span span_of(const CacheAttend& a, int64_t first, int64_t last
 template <int D, int MT>
 struct State {
   float m[MT], l[MT];  // of this lane's row of each 16; l over this lane's tokens
+  float e[MT];         // LSE: their sum before rounding
   bq_f32x4 o[MT][D / 16];
 };
 // 32 tokens' codes, of the keys or of the values
@@ -228,7 +234,7 @@ struct Queries {
 // 32 tokens from j0 into a wave's state. hard: some of them are hidden from
 // some rows (pos: the positions of the lane's rows; -1: no row). next_k,
 // next_v issue the next step's loads, as soon as this one's codes are used.
-template <int D, int MT, bool CAP, bool FINE, typename Q, typename NextK, typename NextV>
+template <int D, int MT, bool CAP, bool FINE, bool LSE, typename Q, typename NextK, typename NextV>
 __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int j0, bool hard, const int (&pos)[MT], const Q& query,
                                     int g, const Scales& s8, Codes<D>& k, Codes<D>& c, State<D, MT>& st, NextK next_k,
                                     NextV next_v) {
@@ -305,6 +311,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
       const float f = m == st.m[r] ? 1.0f : exp2_(st.m[r] - m);
       st.m[r] = m;
       st.l[r] *= f;
+      if constexpr (LSE) st.e[r] *= f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) st.o[r][i] *= f;
     }
@@ -324,10 +331,12 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
         y[i] = pack_bf16(p[2 * i] - __uint_as_float(w[i] << 16), p[2 * i + 1] - __uint_as_float(high_half(w[i])));
     }
     pf[r] = __builtin_bit_cast(ca_bf16x8, w);
+    const auto sum = [&] { return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])); };
     if constexpr (FINE) {
       pl[r] = __builtin_bit_cast(ca_bf16x8, y);
-      st.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      st.l[r] += sum();
     } else {
+      if constexpr (LSE) st.e[r] += sum();
       // of the rounded weights, two an instruction
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.l[r] = add2(w[i], st.l[r]);
@@ -384,7 +393,7 @@ __device__ inline void attend_group(const CacheAttend& a, const Scores& sc, int 
 }
 
 // `steps` times 32 tokens, from j on every `step`, into a wave's state
-template <int D, int MT, bool CAP, bool FINE, typename Q>
+template <int D, int MT, bool CAP, bool FINE, bool LSE, typename Q>
 __device__ inline void walk(const CacheAttend& a, const Scores& sc, const Tile& t, int64_t j, int64_t to, int step, int steps,
                             const int (&pos)[MT], const Q& query, int lane, State<D, MT>& st) {
   Blocks bl = blocks_of(a, t, j, to, step, lane);
@@ -400,7 +409,7 @@ __device__ inline void walk(const CacheAttend& a, const Scores& sc, const Tile& 
     if (next == 0 && more) bl = blocks_of(a, t, j + (int64_t)(n + 1) * step, to, step, lane);
     // hidden from somebody: the rows' positions are first .. last
     const bool hard = uni((int)(!s8.there[0] || !s8.there[1] || j0 + 31 > t.first || (a.window > 0 && t.last >= a.window && j0 <= t.last - a.window)));
-    attend_group<D, MT, CAP, FINE>(a, sc, j0, hard, pos, query, lane >> 4, s8, k, v, st, next_k, next_v);
+    attend_group<D, MT, CAP, FINE, LSE>(a, sc, j0, hard, pos, query, lane >> 4, s8, k, v, st, next_k, next_v);
   }
 }
 
@@ -411,10 +420,10 @@ struct Space {
   int4* heads;  // [share]: parts of the tile that starts in it and ends in a later one, sequence, head, first row
 };
 
-template <int D, int MT>
+template <int D, int MT, bool LSE = false>
 struct Shared {
   float acc[kWaves][4][D / 16 < 8 ? D / 16 : 8][64];
-  float ml[kWaves][2][16 * MT];
+  float ml[kWaves][LSE ? 3 : 2][16 * MT];
   ca_u32x4 q[MT > 1 ? MT : 1][MT > 1 ? D / 32 : 1][MT > 1 ? 64 : 1];
 };
 template <int D>
@@ -439,15 +448,15 @@ __device__ inline ca_u32x4 query_at(const CacheAttend& a, const Scores& sc, cons
 }
 
 // The waves' sums (their maxima and sums are in sh.ml already) joined and written
-template <int D, int MT>
-__device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& ws, int slot, Shared<D, MT>& sh,
+template <int D, int MT, bool LSE>
+__device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& ws, int slot, Shared<D, MT, LSE>& sh,
                               const State<D, MT>& st, int lane, int wave) {
   constexpr int R = 16 * MT, W = D / 16, C = W < 8 ? W : 8;
   const int lo16 = lane & 15, g = lane >> 4, rows = t.s.n * a.group;
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
     const int row = 16 * r + lo16;
-    float m = sh.ml[0][0][row], sum = 0, f[kWaves];
+    float m = sh.ml[0][0][row], sum = 0, before = 0, f[kWaves];  // before rounding
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.ml[w][0][row]);
 #pragma unroll
@@ -455,6 +464,7 @@ __device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& 
       const float mw = sh.ml[w][0][row];
       f[w] = mw == m ? 1.0f : exp2_(mw - m);
       sum += sh.ml[w][1][row] * f[w];
+      if constexpr (LSE) before += sh.ml[w][2][row] * f[w];
     }
     const bool have = t.r0 + row < rows;
     const int tok = (t.r0 + row) / a.group, head = t.h * a.group + (t.r0 + row) % a.group;
@@ -494,7 +504,7 @@ __device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& 
         ws.sums[((int64_t)slot * R + row) * 2] = m;
         ws.sums[((int64_t)slot * R + row) * 2 + 1] = sum;
       } else if (a.lse) {
-        a.lse[tr * a.q_heads + head] = lse_of(m, sum);
+        a.lse[tr * a.q_heads + head] = lse_of(m, LSE ? before : sum);
       }
     }
   }
@@ -503,9 +513,9 @@ __device__ inline void finish(const CacheAttend& a, const Tile& t, const Space& 
 
 // The tile's tokens from .. to (from a multiple of 32): its output, or with
 // slot >= 0 a part of it.
-template <int D, int MT, bool CAP, bool FINE>
+template <int D, int MT, bool CAP, bool FINE, bool LSE>
 __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t from, int64_t to, const Space& ws, int slot,
-                                Shared<D, MT>& sh) {
+                                Shared<D, MT, LSE>& sh) {
   constexpr int W = D / 16;
   const Scores sc = scores_of(a, CAP);
   int lane = threadIdx.x & 63;
@@ -524,7 +534,7 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
     const int row = t.r0 + 16 * r + lo16;
     pos[r] = row < rows ? (int)t.s.p0 + row / a.group : -1;
     st.m[r] = -__builtin_inff();
-    st.l[r] = 0;
+    st.l[r] = st.e[r] = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) st.o[r][i] = (bq_f32x4){0, 0, 0, 0};
   }
@@ -537,8 +547,8 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
       sh.q[n / (D / 32)][n % (D / 32)][lane] = query_at<D>(a, sc, t, t.r0 + 16 * (n / (D / 32)) + lo16, n % (D / 32), g);
     __syncthreads();
   }
-  if constexpr (MT == 1) walk<D, MT, CAP, FINE>(a, sc, t, j, to, kStep, steps, pos, mine, lane, st);
-  else walk<D, MT, CAP, FINE>(a, sc, t, j, to, kStep, steps, pos, LdsQueries<D>{&sh.q[0][0][0], lane}, lane, st);
+  if constexpr (MT == 1) walk<D, MT, CAP, FINE, LSE>(a, sc, t, j, to, kStep, steps, pos, mine, lane, st);
+  else walk<D, MT, CAP, FINE, LSE>(a, sc, t, j, to, kStep, steps, pos, LdsQueries<D>{&sh.q[0][0][0], lane}, lane, st);
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
     const float l = quad_sum(st.l[r]);
@@ -546,12 +556,16 @@ __device__ inline void run_tile(const CacheAttend& a, const Tile& t, int64_t fro
       sh.ml[wave][0][16 * r + lane] = st.m[r];
       sh.ml[wave][1][16 * r + lane] = l;
     }
+    if constexpr (LSE) {
+      const float e = quad_sum(st.e[r]);
+      if (lane < 16) sh.ml[wave][2][16 * r + lane] = e;
+    }
   }
   __syncthreads();
   // what follows is computed here, and not held in registers through the loop
   int lane_ = lane;
   asm volatile("" : "+v"(lane_));
-  finish<D, MT>(a, t, ws, slot, sh, st, lane_, wave);
+  finish(a, t, ws, slot, sh, st, lane_, wave);
 }
 
 // A share is counted in units of 128 2^shift tokens (so that all of a call's
@@ -644,14 +658,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_shares_kernel(
         const int64_t lo = n.from + ((int64_t)(first ? 0 : k0 - kBegin) * kStep << shift);
         const int64_t hi = n.from + ((int64_t)(k1 - kBegin) * kStep << shift);
         const int64_t from = lo > own.from ? lo : own.from, to = hi < own.to ? hi : own.to;
-        run_tile<D, MT, CAP, true>(a, t, from, to, ws, whole ? -1 : 2 * (int)blockIdx.x + first, sh);
+        run_tile<D, MT, CAP, true, false>(a, t, from, to, ws, whole ? -1 : 2 * (int)blockIdx.x + first, sh);
         if (first && !whole)
           open = make_int4(1 + (u + (n.units - k0) - 1) / share - (int)blockIdx.x, seq, t.h, t.r0);
       } else if (n.units == kBegin) {
         // it sees nothing
         Tile t;
         tile_at<R>(a, seq, s, at, h, t);
-        if (k1 == n.units) run_tile<D, MT, CAP, true>(a, t, 0, 0, ws, -1, sh);
+        if (k1 == n.units) run_tile<D, MT, CAP, true, false>(a, t, 0, 0, ws, -1, sh);
       }
       u += k1 - k0;
       k0 = 0;
@@ -732,14 +746,14 @@ __device__ inline bool tile_of(const CacheAttend& a, int64_t v, int h, Tile& t) 
 
 // More rows: a workgroup takes a tile, its waves sharing out the tokens; the
 // last tiles, which see most, go first.
-template <int D, int MT, bool CAP>
+template <int D, int MT, bool CAP, bool LSE>
 __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_tiles_kernel(CacheAttend a) {
-  __shared__ Shared<D, MT> sh;
+  __shared__ Shared<D, MT, LSE> sh;
   const int64_t v = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
   Tile t;
   if (!tile_of<16 * MT>(a, v, (int)((gridDim.x - 1 - blockIdx.x) % a.c.heads), t)) return;
   const Span s = span_of(a, t.first, t.last);
-  run_tile<D, MT, CAP, false>(a, t, s.from, s.to, Space{}, -1, sh);
+  run_tile<D, MT, CAP, false, LSE>(a, t, s.from, s.to, Space{}, -1, sh);
 }
 
 // Many rows: a wave takes a tile with all its tokens, without a word to the
@@ -747,7 +761,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_tiles_kernel(C
 // others find in the CU's cache. Prompts of 1501 to 6007 tokens, 64 query and
 // 8 key heads (8600 tiles): 708 us, by the kernel above 811; one of 4096, 32
 // heads each with its own keys (2080 tiles, a single round here): 190 and 175.
-template <int D, int MT, bool CAP>
+template <int D, int MT, bool CAP, bool LSE>
 __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_rows_kernel(CacheAttend a) {
   constexpr int R = 16 * MT, W = D / 16;
   __shared__ ca_u32x4 queries[kWaves][MT * (D / 32) * 64];
@@ -771,7 +785,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_rows_kernel(Ca
     const int row = t.r0 + 16 * r + lo16;
     pos[r] = row < rows ? (int)t.s.p0 + row / a.group : -1;
     st.m[r] = -__builtin_inff();
-    st.l[r] = 0;
+    st.l[r] = st.e[r] = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) st.o[r][i] = (bq_f32x4){0, 0, 0, 0};
   }
@@ -779,13 +793,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_rows_kernel(Ca
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  walk<D, MT, CAP, false>(a, sc, t, from, to, kGroup, (int)((to - from + kGroup - 1) / kGroup), pos,
+  walk<D, MT, CAP, false, LSE>(a, sc, t, from, to, kGroup, (int)((to - from + kGroup - 1) / kGroup), pos,
                           LdsQueries<D>{queries[wave], lane}, lane, st);
   int lane_ = lane;
   asm volatile("" : "+v"(lane_));  // computed here, and not held in registers through the loop
 #pragma unroll
   for (int r = 0; r < MT; ++r) {
     const float sum = quad_sum(st.l[r]), inv = sum == 0 ? 0.0f : 1.0f / sum;
+    float before = 0;
+    if constexpr (LSE) before = quad_sum(st.e[r]);
     const int row = t.r0 + 16 * r + (lane_ & 15);
     if (row >= rows) continue;
     const int head = t.h * a.group + row % a.group;
@@ -797,7 +813,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_rows_kernel(Ca
       for (int i = 0; i < W; i += 4)
         *(bq_u32x2_a2*)(out + W * k + i) = (bq_u32x2){pack_bf16(st.o[r][i][k] * inv, st.o[r][i + 1][k] * inv),
                                                       pack_bf16(st.o[r][i + 2][k] * inv, st.o[r][i + 3][k] * inv)};
-    if (a.lse && lane_ < 16) a.lse[tr * a.q_heads + head] = lse_of(st.m[r], sum);
+    if constexpr (LSE)
+      if (lane_ < 16) a.lse[tr * a.q_heads + head] = lse_of(st.m[r], before);
   }
 }
 
@@ -846,21 +863,24 @@ Space space_of(void* ws, const Form& f, int head_dim, size_t* bytes) {
   return {(float*)p, (float*)(p + parts), (int4*)(p + parts + sums)};
 }
 
+template <int D, int MT, bool CAP, bool LSE>
+hipError_t run_tiles(const CacheAttend& a, const Form& f, hipStream_t st) {
+  const dim3 block(64 * kWaves);
+  if (f.count >= kRowsTiles) {
+    const unsigned grid = (unsigned)((f.count / a.c.heads + kWaves - 1) / kWaves * a.c.heads);
+    cache_attention_rows_kernel<D, MT, CAP, LSE><<<grid, block, 0, st>>>(a);
+  } else {
+    cache_attention_tiles_kernel<D, MT, CAP, LSE><<<(unsigned)f.count, block, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
 template <int D, int MT>
 hipError_t run(const CacheAttend& a, const Form& f, const Space& ws, hipStream_t st) {
   const dim3 block(64 * kWaves);
   if constexpr (MT == most_rows(D)) {
-    if (f.tiles && f.count >= kRowsTiles) {
-      const unsigned grid = (unsigned)((f.count / a.c.heads + kWaves - 1) / kWaves * a.c.heads);
-      if (a.cap > 0) cache_attention_rows_kernel<D, MT, true><<<grid, block, 0, st>>>(a);
-      else cache_attention_rows_kernel<D, MT, false><<<grid, block, 0, st>>>(a);
-      return hipGetLastError();
-    }
-    if (f.tiles) {
-      if (a.cap > 0) cache_attention_tiles_kernel<D, MT, true><<<(unsigned)f.count, block, 0, st>>>(a);
-      else cache_attention_tiles_kernel<D, MT, false><<<(unsigned)f.count, block, 0, st>>>(a);
-      return hipGetLastError();
-    }
+    if (f.tiles && a.cap > 0) return a.lse ? run_tiles<D, MT, true, true>(a, f, st) : run_tiles<D, MT, true, false>(a, f, st);
+    if (f.tiles) return a.lse ? run_tiles<D, MT, false, true>(a, f, st) : run_tiles<D, MT, false, false>(a, f, st);
   }
   if (a.cap > 0) cache_attention_shares_kernel<D, MT, true><<<f.shares, block, 0, st>>>(a, ws, f.shift);
   else cache_attention_shares_kernel<D, MT, false><<<f.shares, block, 0, st>>>(a, ws, f.shift);
