@@ -198,7 +198,10 @@ class InferenceAttention(torch.nn.Module):
     keys and values, rotation and append, attention, output projection. Wqkv
     [hidden, (heads + 2 kv_heads) head_dim] (queries, keys, values) and Wo
     [heads head_dim, hidden] are stored once, in 8 bits (a scale for each 128
-    elements) or 4 (for each 32). Like them freqs stay as they are, float32,
+    elements) or 4 (for each 32). Of 4 bits the projection's products are
+    exact, and so are the cache's codes but for 1 in 10^6; of 8 bits they are
+    fp8_block_linear_fwd_cached's, which leaves 1 in 1000 of the cache's values
+    a step of their 8 bits off (0.001 of them, rms). Like the weights freqs stay as they are, float32,
     when the module's type is changed."""
 
     def __init__(self, Wqkv: torch.Tensor, Wo: torch.Tensor, heads: int, kv_heads: int, head_dim: int,
