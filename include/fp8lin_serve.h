@@ -53,7 +53,8 @@ extern "C" {
  * negative length counts as 0):
  * nothing is stored for it, it is read as zeros, and attention does not see
  * it. So a padded sequence is one of length 0.
- * Two sequences may share pages that neither appends to.
+ * Sequences may share pages that none appends to; those of the call's own
+ * tokens are each named once.
  */
 typedef struct fp8_cache {
   uint8_t* k;
@@ -126,10 +127,13 @@ fp8_status fp8_cache_read(const fp8_cache* cache, const fp8_cache_batch* batch, 
  * and values enter the products exactly, sums and the softmax are 32-bit, out
  * is bf16 (any strides), lse fp32 [tokens, q_heads] or NULL. Weights enter as
  * two bf16 each, 2^-17 off, so that out is as far off as its own rounding;
- * of prompts large enough to wait for the products and not for memory
- * (FP8_CACHE_TILES and _ROWS) as one, 2^-9 off; lse is the 32-bit weights'
- * in every form. A NaN in a key or value
- * reaches the queries that see it and no others.
+ * in FP8_CACHE_TILES and _ROWS, the forms of batches of many rows, which wait
+ * for the products and not for memory, as one, 2^-9 off. The form is the whole
+ * batch's, by its mean rows: a decoded token beside a prompt's chunk is
+ * computed like the chunk, and much slower over a long context than in a call
+ * of its own. lse is the 32-bit weights' in every form. Products beyond the
+ * 32-bit range count as infinite. A NaN in a key or value reaches the queries
+ * that see it and no others.
  *   ws: fp8_cache_attention_workspace_bytes of the same cache and batch
  *   (their sizes alone count), 16-B aligned; it holds nothing between calls.
  */
@@ -169,14 +173,6 @@ fp8_status fp4_quantize(const void* W_bf16, int64_t ldw, int64_t K, int64_t N, u
 /* Its values in bf16 (exact within its normal range, 2^128 an infinity), row pitch ldw. */
 fp8_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, void* W_bf16, int64_t ldw,
                           hipStream_t stream);
-/*
- * Y [M, N] (dense) = X [M, K] W on a stored 4-bit W. X is quantised as by
- * fp8_block_quantize (E4M3, a scale for each 128 of a row). exact: products
- * are exact and their sums 32-bit, for a Y that is rounded to 8 bits next.
- * Without it products of more than 32 rows are fp8_block_gemm's, up to twice
- * as fast and 1.5e-5 off, which a bf16 Y does not show; of fewer they are
- * exact all the same. Y does not overlap X. scratch: fp4_linear_bytes (0: none is needed).
- */
 /* How a product is cut: the kernel, its wave's 16-row and 16-column tiles and
  * the groups of waves that share K. For profiles and tests. */
 #define FP4_FUSED 0 /* X quantised by the product's launch */
@@ -184,6 +180,15 @@ fp8_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t K
 #define FP4_MANY 2
 #define FP4_EXACT 3 /* many rows, exact products */
 fp8_status fp4_linear_plan(int64_t M, int64_t K, int64_t N, int exact, int* form, int* row_tiles, int* col_tiles, int* groups);
+/*
+ * Y [M, N] (dense) = X [M, K] W on a stored 4-bit W. X is quantised as by
+ * fp8_block_quantize (E4M3, a scale for each 128 of a row). exact: products
+ * are exact and their sums 32-bit, for a Y that is rounded to 8 bits next.
+ * Without it products of more than 32 rows are fp8_block_gemm's, up to twice
+ * as fast and 1.5e-5 off, which a bf16 Y does not show; of fewer they are
+ * exact all the same. Y does not overlap X. scratch: fp4_linear_bytes (0: none
+ * is needed).
+ */
 size_t fp4_linear_bytes(int64_t M, int64_t K, int64_t N);
 fp8_status fp4_linear_fwd_cached(const void* X_bf16, int64_t ldx, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                                  const uint8_t* scales, int exact, void* scratch, size_t scratch_bytes,
